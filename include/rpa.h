@@ -431,6 +431,115 @@ RPA_API int rpa_host_groups(const int32_t *cu_q_lens, int32_t num_seqs,
                             const rpa_dims *dims, int32_t with_lse,
                             int32_t *bounds, int32_t *num_groups);
 
+/* ------------------------------------------------------------------------
+ * The 8-bit K/V cache: half the bytes of a bf16 cache, for decode batches
+ * that are bound by reading it.  rpa_q8_write quantises new rows into their
+ * pages, rpa_q8_read brings rows back, rpa_q8_attend attends over the pages.
+ *
+ * Format.  A row (one token, one KV head, D values x_d) is stored as D codes
+ * and one scale 2^e: e is the smallest integer >= -127 with max_d |x_d| <=
+ * 448 * 2^e (0 for a row of zeros) and code_d = x_d * 2^-e rounded to the
+ * nearest e4m3 value, ties to even.  x_d * 2^-e is exact, so a code is off by one
+ * rounding: at most 2^-4 of the value, or 2^-10 * 2^e for values below
+ * 2^-6 * 2^e.  The row stands for code_d * 2^e.  A row with an infinity or a
+ * NaN gets the NaN scale and zero codes: it stands for NaN throughout.  Codes
+ * written by the library are never NaN; what the operators make of a NaN code
+ * (0x7f, 0xff) that something else wrote is unspecified.
+ *
+ * The lengths stay in device memory, as in rpa_forward_device: cu_q_lens
+ * [max_seqs + 1], kv_lens [max_seqs] and num_seqs [1] are device int32 arrays
+ * read when the kernels run (entries past num_seqs are not read), page_table
+ * is a device array of max_seqs rows, dims->total_q_tokens is the capacity T of
+ * the token arrays (cu_q_lens[num_seqs] <= T), and rows from
+ * cu_q_lens[num_seqs] on are neither read nor written.  What is launched
+ * depends on pointers, dims, max_seqs (and max_q_len) only, nothing is
+ * allocated and the host never waits: every call can be captured into a CUDA
+ * graph and replayed while the lengths and the data change.
+ *
+ * dims->dtype is the type of the arrays outside the cache (RPA_BF16 or
+ * RPA_F32); head_dim, page_size and G are limited as in rpa_forward.  Token
+ * arrays and codes must be 16-byte aligned (RPA_ERR_INVALID_ARG otherwise).
+ * dev_flags: device uint32 that receives RPA_DEV_* bits (OR-ed in, never
+ * cleared), or NULL to drop them.  Lengths that break a rule set
+ * RPA_DEV_BAD_LENGTHS and the call writes nothing else; a page-table entry
+ * outside [0, num_pages) sets RPA_DEV_BAD_PAGE, is read as zeros and not
+ * written.  max_seqs == 0 or T == 0 is a successful no-op.
+ */
+typedef struct {
+  void *k_codes;   /* e4m3 [num_pages, P, Hkv, D] */
+  void *v_codes;
+  void *k_scales;  /* e8m0 (the byte e + 127; 255 is NaN) [num_pages, Hkv, P] */
+  void *v_scales;
+} rpa_q8_cache;
+
+/*
+ * rpa_q8_write -- quantise the new tokens' K and V into their pages.
+ *
+ *   k_new, v_new [T, Hkv, D]: row cu_q_lens[s] + i goes to position
+ *   kv_len[s] - q_len[s] + i of sequence s (kv_len[s] >= q_len[s]).
+ * dims->num_q_heads is checked and otherwise unused.  Slots of other
+ * positions keep their bytes.  Two rows of one call must not share a slot.
+ */
+RPA_API int rpa_q8_write(const void *k_new, const void *v_new,
+                         const rpa_q8_cache *cache, const int32_t *page_table,
+                         const int32_t *cu_q_lens, const int32_t *kv_lens,
+                         const int32_t *num_seqs, int32_t max_seqs,
+                         const rpa_dims *dims, uint32_t *dev_flags,
+                         void *stream);
+
+/*
+ * rpa_q8_read -- the inverse: the last cu_lens[s+1] - cu_lens[s] positions
+ * of sequence s, up to kv_len[s], into rows cu_lens[s] .. of k_out and v_out
+ * [T, Hkv, D], each value code * 2^e rounded to nearest-even (exact in both
+ * types unless it falls below their normal range).
+ */
+RPA_API int rpa_q8_read(void *k_out, void *v_out, const rpa_q8_cache *cache,
+                        const int32_t *page_table, const int32_t *cu_lens,
+                        const int32_t *kv_lens, const int32_t *num_seqs,
+                        int32_t max_seqs, const rpa_dims *dims,
+                        uint32_t *dev_flags, void *stream);
+
+/*
+ * rpa_q8_workspace_size -- bytes of device workspace rpa_q8_attend needs for
+ * at most max_seqs sequences of at most max_q_len new tokens under dims.
+ * Host only; RPA_OK or the RPA_ERR_* code of bad dims, max_seqs or max_q_len
+ * (then *bytes = 0).
+ */
+RPA_API int rpa_q8_workspace_size(const rpa_dims *dims, int32_t max_seqs,
+                                  int32_t max_q_len, int64_t *bytes);
+
+/*
+ * rpa_q8_attend -- exact attention of ragged queries over the cached keys.
+ *
+ *   q, out [T, Hq, D], lse [T, Hq] float32 or NULL.  Query row cu_q_lens[s] + i,
+ *   head h sees positions j < kv_len[s] of KV head h / G and, when causal != 0,
+ *   only j <= kv_len[s] - q_len[s] + i (aligned to the end):
+ *   out = sum_j softmax_j(scale * q.k_j) v_j and lse = ln sum_j exp(scale *
+ *   q.k_j) with k_j, v_j the values that the cached rows stand for, held in
+ *   fp32 and out rounded once.
+ *   The keys are all in the cache: new tokens are written by rpa_q8_write
+ *   first and attended to as stored.  Any kv_len >= 0 is allowed for any
+ *   q_len: with causal == 0 this is cross attention to cached states of
+ *   another length.  A row that sees no key gets out = 0 and lse = -inf.  A
+ *   row that sees a token whose K or V row stands for NaN gets NaN in out and
+ *   lse; a token outside a row's mask never reaches it.
+ * max_q_len: no q_len of the batch is above it (else RPA_DEV_BAD_LENGTHS).
+ *   With max_q_len == 1 only the single-token kernel is launched.
+ * workspace: caller-owned device memory, 256-byte aligned, of at least
+ *   rpa_q8_workspace_size bytes, else RPA_ERR_WORKSPACE.  Its contents need no
+ *   initialisation and mean nothing after the call; calls that share one must
+ *   be ordered on the device (two graphs that may run at once need two).
+ * out and lse must not overlap any input.
+ */
+RPA_API int rpa_q8_attend(const void *q, const rpa_q8_cache *cache,
+                          const int32_t *page_table, const int32_t *cu_q_lens,
+                          const int32_t *kv_lens, const int32_t *num_seqs,
+                          int32_t max_seqs, int32_t max_q_len, float scale,
+                          int32_t causal, void *out, float *lse,
+                          const rpa_dims *dims, void *workspace,
+                          int64_t workspace_bytes, uint32_t *dev_flags,
+                          void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -324,3 +324,138 @@ def rpa_host_groups(cu_q_lens, dims: rpa_dims, with_lse: bool = True) -> np.ndar
     if rc != RPA_OK:
         raise RpaError(rc, "rpa_host_groups")
     return bounds[:n.value + 1].copy()
+
+
+# ---------------------------------------------------------------- 8-bit cache
+class rpa_q8_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_codes", "v_codes", "k_scales", "v_scales")]
+
+
+_C = ctypes.POINTER(rpa_q8_cache)
+_D = ctypes.POINTER(rpa_dims)
+_lib.rpa_q8_write.argtypes = [_P, _P, _C, _P, _P, _P, _P, _i32, _D, _P, _P]
+_lib.rpa_q8_write.restype = ctypes.c_int
+_lib.rpa_q8_read.argtypes = [_P, _P, _C, _P, _P, _P, _P, _i32, _D, _P, _P]
+_lib.rpa_q8_read.restype = ctypes.c_int
+_lib.rpa_q8_workspace_size.argtypes = [_D, _i32, _i32, ctypes.POINTER(ctypes.c_int64)]
+_lib.rpa_q8_workspace_size.restype = ctypes.c_int
+_lib.rpa_q8_attend.argtypes = [_P, _C, _P, _P, _P, _P, _i32, _i32, ctypes.c_float, _i32, _P, _P, _D, _P,
+                               ctypes.c_int64, _P, _P]
+_lib.rpa_q8_attend.restype = ctypes.c_int
+
+
+def _q8_common(rows, k_codes, v_codes, k_scales, v_scales, page_table, cu_lens, kv_lens, num_seqs, dev_flags, stream):
+    """Checks what the three calls share; returns the cache, the dims, the
+    list of device pointers (page_table, cu_lens, kv_lens, num_seqs), max_seqs,
+    the dev_flags and stream pointers, and the device of `rows`."""
+    device = rows.device
+    if k_codes.dim() != 4 or rows.dim() != 3 or page_table.dim() != 2:
+        raise ValueError("the codes have 4 dimensions, the token arrays 3 and page_table 2")
+    num_pages, page_size, hkv, d = k_codes.shape
+    for name, t in (("k_codes", k_codes), ("v_codes", v_codes)):
+        if t.shape != k_codes.shape or t.dtype != torch.float8_e4m3fn:
+            raise TypeError(f"{name} must be float8_e4m3fn {list(k_codes.shape)}, got {t.dtype} {list(t.shape)}")
+    for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+        if t.shape != (num_pages, hkv, page_size) or t.dtype != torch.float8_e8m0fnu:
+            raise TypeError(f"{name} must be float8_e8m0fnu {[num_pages, hkv, page_size]}, got {t.dtype} "
+                            f"{list(t.shape)}")
+    max_seqs = kv_lens.numel()
+    if cu_lens.numel() < max_seqs + 1 or num_seqs.numel() < 1 or page_table.shape[0] < max_seqs:
+        raise ValueError("cu_lens needs max_seqs + 1 entries, num_seqs one, page_table max_seqs rows")
+    if rows.shape[2] != d:
+        raise ValueError(f"head_dim {rows.shape[2]} of the token arrays is not the cache's {d}")
+    named = (("k_codes", k_codes), ("v_codes", v_codes), ("k_scales", k_scales), ("v_scales", v_scales),
+             ("page_table", page_table), ("cu_lens", cu_lens), ("kv_lens", kv_lens), ("num_seqs", num_seqs),
+             ("dev_flags", dev_flags))
+    for name, t in named:
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the token arrays on {device}")
+    cache = rpa_q8_cache(*(_dev(t, name) for name, t in named[:4]))
+    ptrs = [_dev(t, name, torch.int32) for name, t in named[4:8]]
+    dims = rpa_dims(num_q_heads=rows.shape[1], num_kv_heads=hkv, head_dim=d, page_size=page_size,
+                    num_pages=num_pages, max_pages_per_seq=page_table.shape[1], total_q_tokens=rows.shape[0],
+                    dtype=_dtype_code(rows))
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    sptr = ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    return cache, dims, ptrs, max_seqs, _dev(dev_flags, "dev_flags", torch.int32), sptr, device
+
+
+def _q8_call(name, device, *args):
+    """Calls the entry point with `device` current (its kernels launch there)."""
+    if device.index is not None and device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            rc = getattr(_lib, name)(*args)
+    else:
+        rc = getattr(_lib, name)(*args)
+    if rc != RPA_OK:
+        raise RpaError(rc, name)
+
+
+def _same_rows(name, t, like):
+    if t.dtype != like.dtype or t.shape != like.shape or t.device != like.device:
+        raise TypeError(f"{name} must be {like.dtype} {list(like.shape)} on {like.device}, "
+                        f"got {t.dtype} {list(t.shape)} on {t.device}")
+
+
+def rpa_q8_write(k_new, v_new, k_codes, v_codes, k_scales, v_scales, page_table, cu_q_lens, kv_lens, num_seqs,
+                 dev_flags=None, stream=None) -> None:
+    """Calls rpa_q8_write: quantises the new tokens' K/V rows into their pages.
+
+    CUDA tensors: k_new/v_new [T,Hkv,D] bf16 or fp32, codes float8_e4m3fn
+    [pages,P,Hkv,D], scales float8_e8m0fnu [pages,Hkv,P], page_table
+    [max_seqs,max_pages], cu_q_lens [max_seqs+1], kv_lens [max_seqs] and
+    num_seqs [1] int32.  dev_flags: optional int32 tensor of one element that
+    receives the device error bits."""
+    cache, dims, ptrs, max_seqs, flags, sptr, device = _q8_common(
+        k_new, k_codes, v_codes, k_scales, v_scales, page_table, cu_q_lens, kv_lens, num_seqs, dev_flags, stream)
+    _same_rows("v_new", v_new, k_new)
+    if k_new.shape[1] != dims.num_kv_heads:
+        raise ValueError(f"k_new has {k_new.shape[1]} heads, the cache {dims.num_kv_heads}")
+    _q8_call("rpa_q8_write", device, _dev(k_new, "k_new"), _dev(v_new, "v_new"), ctypes.byref(cache), *ptrs,
+             max_seqs, ctypes.byref(dims), flags, sptr)
+
+
+def rpa_q8_read(k_out, v_out, k_codes, v_codes, k_scales, v_scales, page_table, cu_lens, kv_lens, num_seqs,
+                dev_flags=None, stream=None) -> None:
+    """Calls rpa_q8_read: the last cu_lens[s+1] - cu_lens[s] cached positions
+    of every sequence s into its rows of k_out / v_out [T,Hkv,D] (bf16 or
+    fp32).  The other arguments are rpa_q8_write's."""
+    cache, dims, ptrs, max_seqs, flags, sptr, device = _q8_common(
+        k_out, k_codes, v_codes, k_scales, v_scales, page_table, cu_lens, kv_lens, num_seqs, dev_flags, stream)
+    _same_rows("v_out", v_out, k_out)
+    if k_out.shape[1] != dims.num_kv_heads:
+        raise ValueError(f"k_out has {k_out.shape[1]} heads, the cache {dims.num_kv_heads}")
+    _q8_call("rpa_q8_read", device, _dev(k_out, "k_out"), _dev(v_out, "v_out"), ctypes.byref(cache), *ptrs,
+             max_seqs, ctypes.byref(dims), flags, sptr)
+
+
+def rpa_q8_workspace_size(dims: rpa_dims, max_seqs: int, max_q_len: int) -> int:
+    """Bytes of device workspace rpa_q8_attend needs for these dims, at most
+    `max_seqs` sequences and at most `max_q_len` new tokens in any of them."""
+    n = ctypes.c_int64(0)
+    rc = _lib.rpa_q8_workspace_size(ctypes.byref(dims), int(max_seqs), int(max_q_len), ctypes.byref(n))
+    if rc != RPA_OK:
+        raise RpaError(rc, "rpa_q8_workspace_size")
+    return int(n.value)
+
+
+def rpa_q8_attend(q, k_codes, v_codes, k_scales, v_scales, page_table, cu_q_lens, kv_lens, num_seqs, max_q_len: int,
+                  scale: float, causal: bool, out, workspace, lse=None, dev_flags=None, stream=None) -> None:
+    """Calls rpa_q8_attend: attention of ragged queries over the 8-bit cache
+    (decode, chunks of new tokens already written, or, with causal False, cross
+    attention to cached states of another length).
+
+    q, out [T,Hq,D] bf16 or fp32, lse [T,Hq] float32 or None, max_q_len: an
+    upper bound of the batch's q_lens, workspace: uint8 CUDA tensor of at least
+    rpa_q8_workspace_size bytes.  The other arguments are rpa_q8_write's."""
+    cache, dims, ptrs, max_seqs, flags, sptr, device = _q8_common(
+        q, k_codes, v_codes, k_scales, v_scales, page_table, cu_q_lens, kv_lens, num_seqs, dev_flags, stream)
+    _same_rows("out", out, q)
+    if lse is not None and (tuple(lse.shape) != tuple(q.shape[:2]) or lse.device != device):
+        raise ValueError(f"lse must be {list(q.shape[:2])} on {device}")
+    if workspace.device != device:
+        raise ValueError(f"workspace is on {workspace.device}, the token arrays on {device}")
+    _q8_call("rpa_q8_attend", device, _dev(q, "q"), ctypes.byref(cache), *ptrs, max_seqs, int(max_q_len),
+             float(scale), int(bool(causal)), _dev(out, "out"), _dev(lse, "lse", torch.float32), ctypes.byref(dims),
+             _dev(workspace, "workspace", torch.uint8), workspace.numel(), flags, sptr)
