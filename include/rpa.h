@@ -458,7 +458,8 @@ RPA_API int rpa_host_groups(const int32_t *cu_q_lens, int32_t num_seqs,
  *
  * dims->dtype is the type of the arrays outside the cache (RPA_BF16 or
  * RPA_F32); head_dim, page_size and G are limited as in rpa_forward.  Token
- * arrays and codes must be 16-byte aligned (RPA_ERR_INVALID_ARG otherwise).
+ * arrays, codes and scales must be 16-byte aligned (RPA_ERR_INVALID_ARG
+ * otherwise).
  * dev_flags: device uint32 that receives RPA_DEV_* bits (OR-ed in, never
  * cleared), or NULL to drop them.  Lengths that break a rule set
  * RPA_DEV_BAD_LENGTHS and the call writes nothing else; a page-table entry

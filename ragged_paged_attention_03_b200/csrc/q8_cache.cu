@@ -179,7 +179,8 @@ int io_call(void *k, void *v, const rpa_q8_cache *cache, const int32_t *page_tab
   if (!k || !v || !cache || !cache->k_codes || !cache->v_codes || !cache->k_scales || !cache->v_scales ||
       !page_table || !cu || !kv || !num_seqs)
     return RPA_ERR_INVALID_ARG;
-  if (!aligned16(k) || !aligned16(v) || !aligned16(cache->k_codes) || !aligned16(cache->v_codes))
+  if (!aligned16(k) || !aligned16(v) || !aligned16(cache->k_codes) || !aligned16(cache->v_codes) ||
+      !aligned16(cache->k_scales) || !aligned16(cache->v_scales))
     return RPA_ERR_INVALID_ARG;
   IoArgs a{};
   a.k = k;

@@ -1,0 +1,39 @@
+// q8_kernels.h -- launch interface of the attention kernels on the 8-bit cache.
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "q8_common.cuh"
+#include "rpa.h"
+
+namespace rpa {
+namespace q8 {
+
+// What every attention kernel of a call reads.
+struct AttendArgs {
+  const void *q;
+  Cache c;
+  Lengths len;
+  const int32_t *page_table;
+  uint32_t *err;                 // may be null
+  void *out;
+  float *lse;                    // may be null
+  int32_t hq, hkv, p, p_shift, num_pages, max_pages, causal;
+  float scale;
+};
+
+__device__ __forceinline__ void store(float *p, float v) { *p = v; }
+__device__ __forceinline__ void store(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+// Few query rows per KV head.  Sequences with q_len > q_limit are left out.
+int rows_per_group(const rpa_dims &d, int32_t max_q);
+int rows_grid(const rpa_dims &d, int32_t max_seqs, int32_t max_q, int R);
+struct RowsLayout {
+  int64_t heads, ml, o, total;   // byte offsets into the workspace
+};
+RowsLayout rows_layout(int grid, int R, int D);
+cudaError_t launch_rows(const AttendArgs &a, const rpa_dims &d, int32_t max_seqs, int32_t max_q, int32_t q_limit,
+                        uint8_t *ws, cudaStream_t stream);
+
+}  // namespace q8
+}  // namespace rpa

@@ -1,0 +1,968 @@
+// q8_rows_kernel.cu -- attention over the 8-bit cache for few query rows per
+// KV head (single tokens, a few tokens, and every fp32 call): bound by reading
+// the cache once.
+//
+// Mathematics.  A group of R query rows of one KV head (rows are the pairs
+// (token i, head g), row = i * G + g) runs over blocks of 128 keys with the
+// keys on the M side of the tensor cores, so that the codes are used as they lie
+// in the cache, never converted:
+//   S^T[128 keys x R] = K Q^T      A = K codes, K-major, straight from TMA
+//   O^T[D x R]       += V^T P^T    A = V codes, M-major, the same
+// in kind::f8f6f4, whose B operand must be 8 bits too.  Q and the weights P
+// are therefore written as sums of e4m3 parts, part i scaled by 16^i:
+// each part takes 4 bits of the significand, and the remainder of a rounding is
+// exact in fp32, so
+//   bf16 I/O: 2 parts of Q (exact down to 2^-21 of the row's largest |q|),
+//             4 of P (16 bits; weights down to 2^-30 of the largest count, so a
+//             long flat tail behind one large weight keeps its sum);
+//   fp32 I/O: 6 parts of both (24 bits, as the fp32 values they come from).
+// The parts are columns of the same MMA (N = parts * R, whose time below
+// N = 64 is that of reading A), and their products are joined in fp32.
+// Scales: a key's K scale multiplies its score and its V scale its weight; one
+// thread owns one key, so both are a scalar of that thread.  Weights are scaled
+// by 2^(ev - max ev of the block) * 256 before the rounding to parts.
+// Softmax: running maximum and sum in fp32 (log2 domain).  Each block's product
+// O^T is read from TMEM into fp32 registers, which are rescaled when the
+// maximum moves: no read-modify-write of TMEM and no wait between blocks.
+//
+// Split of the work: the blocks of every (sequence, KV head, row group) in a
+// row are one list, cut into equal runs, one per CTA (every SM gets the same
+// number of blocks whatever the lengths).  A CTA computes its run from the
+// lengths in device memory, so there is no planning launch.  A run may begin and
+// end inside a group: those partial results go to the workspace and
+// combine_kernel, queued behind with programmatic dependent launch, joins them
+// in the order of the keys (the same bits every time).
+//
+// Warps: 0-3 softmax, weights and output (thread = key of the block, then row of
+// O^T), 4 TMA of K and V tiles, 5 MMA issue, 6 the parts of Q, 7 the scales
+// (cp.async).  Everything runs ahead across groups through rings in shared
+// memory.
+#include <cuda.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "ptx.cuh"
+#include "q8_common.cuh"
+#include "q8_kernels.h"
+#include "tma.h"
+
+namespace rpa {
+namespace q8 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int BN = 128;               // keys per block
+constexpr int kScaleSlots = 8;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kPartStep = 1.f / 16.f;
+
+template <typename T> struct Parts;
+template <> struct Parts<__nv_bfloat16> { static constexpr int Q = 2, P = 4; };
+template <> struct Parts<float> { static constexpr int Q = 6, P = 6; };
+
+constexpr int round_up(int x, int m) { return (x + m - 1) / m * m; }
+constexpr int pow2_cols(int x) { return x <= 32 ? 32 : x <= 64 ? 64 : x <= 128 ? 128 : x <= 256 ? 256 : 512; }
+
+template <typename T, int D, int R>
+struct Shape {
+  static constexpr int NQ = Parts<T>::Q, NP = Parts<T>::P;
+  static constexpr int CQ = NQ * R, CP = NP * R;                 // columns in use
+  static constexpr int NQpad = round_up(CQ, 16), NPpad = round_up(CP, 16);
+  static constexpr int RC = R < 8 ? R : 8;                       // rows read from TMEM at a time
+  static constexpr int W = D == 64 ? 64 : 128;                   // bytes of a tile row
+  static constexpr int CT = D / W;                               // column tiles
+  static constexpr int kTile = BN * D;                           // K or V codes of a block
+  static constexpr int kQBuf = NQpad * D;
+  static constexpr int kPBuf = NPpad * BN;
+  static constexpr int kFixed = 1024 + 2 * kQBuf + 2 * kPBuf + kScaleSlots * 2 * BN + 2560;
+  static constexpr int kTmem = pow2_cols(2 * NQpad + 2 * NPpad * CT);
+  // CTAs per SM: three where their TMEM, registers and two-slot rings fit
+  static constexpr int kSmMax = 227 * 1024;
+  static constexpr int fits(int ctas, int ns) {
+    return ctas * (kFixed + 2 * ns * kTile + 1024) <= kSmMax && ctas * kTmem <= 512 ? 1 : 0;
+  }
+  static constexpr int CTAS = R <= 4 && fits(3, 2) ? 3 : fits(2, 2) ? 2 : 1;
+  static constexpr int slots() {
+    int ns = 2;
+    while (ns < 8 && fits(CTAS, ns + 1)) ++ns;
+    return ns;
+  }
+  static constexpr int NS = slots();
+  static constexpr int kSmem = kFixed + 2 * NS * kTile;
+  static_assert(fits(1, 2) == 1, "shape does not fit");
+};
+
+struct Bars {
+  uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8];
+  uint64_t s_full[2], p_full[2], pv_full[2];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots];
+  uint64_t x_full[2], l_full;    // the softmax warps' maxima and sums are in shared memory
+  uint64_t drain;
+};
+
+// A partial result of a group: its CTA's run begins or ends inside the group.
+struct PartHead {
+  int32_t seq, hk, grp, begin;   // begin: first block of the run in the group (> 0: joined by the combine)
+};
+
+struct Args {
+  AttendArgs a;
+  int32_t q_limit;               // longer sequences are another kernel's
+  PartHead *heads;               // [ctas]
+  float *ml;                     // [2 * ctas][R][2] running maximum (log2) and sum
+  float *o;                      // [2 * ctas][R][D] unnormalised
+};
+
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort_flag, uint32_t *err) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer();
+  while (!ptx::mbar_try_wait(bar, parity)) {
+    if (*abort_flag) return false;
+    if (ptx::globaltimer() - t0 > ptx::kWaitLimitNs) {
+      *abort_flag = 1;
+      raise(err, RPA_DEV_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort_flag, uint32_t *err) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, err));
+}
+
+// Blocks of one sequence: groups of R rows per KV head, each of nb blocks (a
+// sequence without keys has one, empty, so that its rows are written).
+struct SeqWork {
+  int groups, nb;
+  __device__ __forceinline__ int64_t blocks(int hkv) const { return (int64_t)groups * hkv * nb; }
+};
+template <int R>
+__device__ __forceinline__ SeqWork seq_work(int q_len, int kv_len, int G, int q_limit) {
+  SeqWork w;
+  w.groups = q_len > q_limit ? 0 : (q_len * G + R - 1) / R;
+  w.nb = max(1, (kv_len + BN - 1) / BN);
+  return w;
+}
+
+// The CTA's run of blocks as segments, one per group it touches.
+template <int R>
+struct Run {
+  const AttendArgs *a;
+  int n, G, q_limit;
+  int s, unit, blk;
+  int64_t left;
+  // the current segment
+  int q0, q_len, kv, hk, grp, nb, b0, b1;
+
+  __device__ __forceinline__ bool next() {
+    if (left <= 0) return false;
+    SeqWork w;
+    while (true) {
+      if (s >= n) return false;
+      q0 = a->len.cu[s];
+      q_len = a->len.cu[s + 1] - q0;
+      kv = a->len.kv[s];
+      w = seq_work<R>(q_len, kv, G, q_limit);
+      if (unit < w.groups * a->hkv) break;
+      ++s;
+      unit = 0;
+    }
+    nb = w.nb;
+    hk = unit / w.groups;
+    grp = unit - hk * w.groups;
+    b0 = blk;
+    const int take = (int)(left < nb - blk ? left : nb - blk);
+    b1 = b0 + take;
+    left -= take;
+    blk = 0;
+    ++unit;
+    return true;
+  }
+  // keys seen by row `row` of the group, and by its last row
+  __device__ __forceinline__ int row_end(int row) const {
+    const int rho = grp * R + row;
+    if (rho >= q_len * G) return 0;
+    return a->causal ? min(kv, max(0, kv - q_len + rho / G + 1)) : kv;
+  }
+  // the segment's last block that any row sees, plus one (>= b0)
+  __device__ __forceinline__ int last_block() const {
+    const int rho = min((grp + 1) * R, q_len * G) - 1;
+    const int end = a->causal ? min(kv, max(0, kv - q_len + rho / G + 1)) : kv;
+    const int vis = max(1, (end + BN - 1) / BN);
+    return max(b0, min(b1, vis));
+  }
+};
+
+__device__ __forceinline__ float joined(float m) { return m == -INFINITY ? 0.f : m; }
+
+// Largest of the warp's values (a NaN is passed over, as fmaxf does).
+__device__ __forceinline__ float warp_max(float x) {
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+  return m;
+}
+
+// sum_p 16^-p x part p of RC rows; part p of a row is R columns after part p - 1.
+template <int NP, int R, int RC>
+__device__ __forceinline__ void join_parts(uint32_t taddr, float (&sum)[RC]) {
+  uint32_t v[NP * RC];
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    if constexpr (RC == 8) ptx::tmem_ld8(taddr + p * R, v, p * RC);
+    else ptx::tmem_ld4(taddr + p * R, v, p * RC);
+  }
+  ptx::tmem_ld_wait();
+#pragma unroll
+  for (int r = 0; r < RC; ++r) {
+    sum[r] = __uint_as_float(v[(NP - 1) * RC + r]);
+#pragma unroll
+    for (int p = NP - 2; p >= 0; --p) sum[r] = fmaf(sum[r], kPartStep, __uint_as_float(v[p * RC + r]));
+  }
+}
+
+template <typename T, int D, int R>
+__global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
+    rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Args g) {
+  using S = Shape<T, D, R>;
+  constexpr int NS = S::NS;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *sK = base;
+  uint8_t *sV = sK + NS * S::kTile;
+  uint8_t *sQ = sV + NS * S::kTile;                        // two buffers
+  uint8_t *sP = sQ + 2 * S::kQBuf;                         // two buffers
+  uint8_t *sSc = sP + 2 * S::kPBuf;                        // [slot][K, V][128]
+  Bars *bars = reinterpret_cast<Bars *>(sSc + kScaleSlots * 2 * BN);
+  float *s_qf = reinterpret_cast<float *>(bars + 1);       // [2][16] row factors
+  int *s_end = reinterpret_cast<int *>(s_qf + 32);         // [2][16] keys each row sees
+  float *s_max = reinterpret_cast<float *>(s_end + 32);    // [2][4][16] warps' maxima
+  int *s_ev = reinterpret_cast<int *>(s_max + 128);        // [2][4] warps' largest V scale
+  float *s_l = reinterpret_cast<float *>(s_ev + 8);        // [4][16]
+  int64_t *s_scan = reinterpret_cast<int64_t *>(s_l + 64); // [8 + 3]
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_scan + 12);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+  const AttendArgs &a = g.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cta = blockIdx.x, ctas = gridDim.x;
+  const int G = a.hq / a.hkv;
+
+  // ---- this CTA's run of blocks
+  const int n = checked_seqs(a.len);
+  if (n < 0) {
+    if (cta == 0 && tid == 0) raise(a.err, RPA_DEV_BAD_LENGTHS);
+    if (tid == 0) g.heads[cta].begin = 0;
+    return;
+  }
+  int64_t mine = 0;
+  for (int s = tid; s < n; s += kThreads)
+    mine += seq_work<R>(a.len.cu[s + 1] - a.len.cu[s], a.len.kv[s], G, g.q_limit).blocks(a.hkv);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) s_scan[warp] = mine;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) total += s_scan[w];
+  // equal runs: the first `total % ctas` CTAs take one block more
+  const int64_t per = total / ctas, extra = total - per * ctas;
+  const int64_t first = per * cta + (cta < extra ? cta : extra);
+  const int64_t count = per + (cta < extra ? 1 : 0);
+  if (count == 0) {
+    if (tid == 0) g.heads[cta].begin = 0;
+    return;
+  }
+  // the sequence holding block `first`: a scan over the sequences, 256 at a time
+  int64_t before = 0;
+  for (int s0 = 0; s0 < n; s0 += kThreads) {
+    const int s = s0 + tid;
+    SeqWork w{0, 1};
+    if (s < n) w = seq_work<R>(a.len.cu[s + 1] - a.len.cu[s], a.len.kv[s], G, g.q_limit);
+    const int64_t b = w.blocks(a.hkv);
+    int64_t incl = b;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    __syncthreads();                    // s_scan of the previous round has been read
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    int64_t excl = before + incl - b;
+    int64_t round = 0;
+#pragma unroll
+    for (int w2 = 0; w2 < kThreads / 32; ++w2) {
+      if (w2 < warp) excl += s_scan[w2];
+      round += s_scan[w2];
+    }
+    if (first >= excl && first < excl + b) {
+      const int64_t off = first - excl;
+      s_scan[8] = s;
+      s_scan[9] = off / w.nb;
+      s_scan[10] = off % w.nb;
+    }
+    before += round;
+    if (first < before) break;          // uniform
+  }
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      ptx::mbar_init(&bars->k_full[i], 1);
+      ptx::mbar_init(&bars->k_empty[i], 1);
+      ptx::mbar_init(&bars->v_full[i], 1);
+      ptx::mbar_init(&bars->v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&bars->s_full[i], 1);
+      ptx::mbar_init(&bars->p_full[i], 128);
+      ptx::mbar_init(&bars->pv_full[i], 1);
+      ptx::mbar_init(&bars->q_full[i], 32);
+      ptx::mbar_init(&bars->q_empty[i], 1 + 128);   // the last QK's commit and the softmax threads
+    }
+    for (int i = 0; i < kScaleSlots; ++i) {
+      ptx::mbar_init(&bars->sc_full[i], 32);
+      ptx::mbar_init(&bars->sc_empty[i], 128);
+    }
+    ptx::mbar_init(&bars->x_full[0], 4);
+    ptx::mbar_init(&bars->x_full[1], 4);
+    ptx::mbar_init(&bars->l_full, 4);
+    ptx::mbar_init(&bars->drain, 1);
+    *abort_flag = 0;
+    ptx::fence_barrier_init();
+  }
+  if (warp == 5) {
+    ptx::tmem_alloc(tmem_slot, S::kTmem);
+    ptx::tmem_relinquish();
+  }
+  if (tid == 128) {
+    ptx::tma_prefetch_desc(&tm_k);
+    ptx::tma_prefetch_desc(&tm_v);
+  }
+  // columns that no part fills are zeros
+  if (S::NQpad > S::CQ)
+    for (int i = tid; i < 2 * S::kQBuf / 16; i += kThreads) reinterpret_cast<uint4 *>(sQ)[i] = make_uint4(0, 0, 0, 0);
+  ptx::fence_proxy_async_smem();
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tS = tmem, tO = tmem + 2 * S::NQpad;
+
+  Run<R> run;
+  run.a = &a;
+  run.n = n;
+  run.G = G;
+  run.q_limit = g.q_limit;
+  run.s = (int)s_scan[8];
+  run.unit = (int)s_scan[9];
+  run.blk = (int)s_scan[10];
+  run.left = count;
+
+  if (warp == 4) {
+    // ------------------------------------------------------------ TMA
+    const uint64_t once = ptx::l2_evict_first_policy();
+    const int br = a.p < BN ? a.p : BN;
+    const int nseg = BN / br;
+    const uint32_t seg_bytes = (uint32_t)(br * D);
+    int gb = 0;
+    bool ok = true;
+    while (ok && run.next()) {
+      const int last = run.last_block();
+      const int32_t *pt = a.page_table + (size_t)run.s * a.max_pages;
+      auto page_of = [&](int b) -> int {
+        const int pos = b * BN + lane * br;
+        return lane < nseg && b < last && pos < run.kv ? pt[pos >> a.p_shift] : -1;
+      };
+      int next_page = page_of(run.b0);
+      for (int b = run.b0; b < last; ++b, ++gb) {
+        const int page = next_page;
+        next_page = page_of(b + 1);
+        const int pos = b * BN + lane * br;
+        const bool load = lane < nseg && pos < run.kv;
+        int row = page * a.p + (pos & (a.p - 1));
+        if (load && (page < 0 || page >= a.num_pages)) {
+          raise(a.err, RPA_DEV_BAD_PAGE);
+          row = a.num_pages * a.p;      // outside the tensor: the copy fills zeros
+        }
+        const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, load)) * seg_bytes;
+        const int st = gb % NS;
+        const uint32_t ph = (uint32_t)((gb / NS) & 1);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          uint64_t *full = kv ? &bars->v_full[st] : &bars->k_full[st];
+          uint64_t *empty = kv ? &bars->v_empty[st] : &bars->k_empty[st];
+          uint8_t *dst = (kv ? sV : sK) + st * S::kTile + lane * br * S::W;
+          if (gb >= NS && !wait_warp(empty, ph ^ 1u, abort_flag, a.err)) {
+            ok = false;
+            break;
+          }
+          ptx::mbar_arrive_expect_tx_elect(full, bytes);
+          __syncwarp();
+          if (load)
+#pragma unroll
+            for (int c = 0; c < S::CT; ++c)
+              ptx::tma_load_3d_hint(dst + c * BN * S::W, kv ? &tm_v : &tm_k, full, c * S::W, run.hk, row, once);
+          __syncwarp();
+        }
+        if (!ok) break;
+      }
+    }
+    // every queued copy lands before the CTA ends
+    if (lane == 0)
+      for (int k = gb - NS < 0 ? 0 : gb - NS; k < gb; ++k) {
+        ptx::mbar_wait(&bars->k_full[k % NS], (uint32_t)((k / NS) & 1));
+        ptx::mbar_wait(&bars->v_full[k % NS], (uint32_t)((k / NS) & 1));
+      }
+    __syncwarp();
+  } else if (warp == 5) {
+    // ------------------------------------------------------------ MMA
+    constexpr uint32_t idesc_qk = ptx::umma_idesc_e4m3(128, S::NQpad, false, false);
+    constexpr uint32_t idesc_pv = ptx::umma_idesc_e4m3(128, S::NPpad, true, true);
+    constexpr uint32_t sw = S::W == 128 ? 2 : 4;
+    const uint64_t dk0 = ptx::umma_desc(ptx::smem_u32(sK), 16, 8 * S::W, sw);
+    const uint64_t dq0 = ptx::umma_desc(ptx::smem_u32(sQ), 16, 8 * S::W, sw);
+    // head_dim 64: rows 64..127 of M read the same 64 values (LBO 0); their lanes are not used
+    const uint64_t dv0 = ptx::umma_desc(ptx::smem_u32(sV), 0, 8 * S::W, sw);
+    const uint64_t dp0 = ptx::umma_desc(ptx::smem_u32(sP), 128, BN * 16, 0);
+    int gb = 0, seg = 0;
+    bool ok = true;
+    // QK of block `blk` (ring position) of the segment in Q buffer `qb`
+    auto qk = [&](int blk, int qb) -> bool {
+      const int st = blk % NS;
+      if (!wait_warp(&bars->k_full[st], (uint32_t)((blk / NS) & 1), abort_flag, a.err)) return false;
+      ptx::tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        const int c = k * 32 / S::W, kk = k * 32 % S::W;
+        ptx::umma_ss_e4m3_elect(tS + (blk & 1) * S::NQpad,
+                                dk0 + (uint64_t)((st * S::kTile + c * BN * S::W + kk) >> 4),
+                                dq0 + (uint64_t)((qb * S::kQBuf + c * S::NQpad * S::W + kk) >> 4), idesc_qk, k > 0);
+      }
+      ptx::umma_commit_elect(&bars->s_full[blk & 1]);
+      ptx::umma_commit_elect(&bars->k_empty[st]);
+      return true;
+    };
+    auto pv = [&](int blk) -> bool {
+      const int st = blk % NS;
+      if (!wait_warp(&bars->p_full[blk & 1], (uint32_t)((blk >> 1) & 1), abort_flag, a.err)) return false;
+      if (!wait_warp(&bars->v_full[st], (uint32_t)((blk / NS) & 1), abort_flag, a.err)) return false;
+      ptx::tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < S::CT; ++c)
+#pragma unroll
+        for (int k = 0; k < BN / 32; ++k)
+          ptx::umma_ss_e4m3_elect(tO + ((blk & 1) * S::CT + c) * S::NPpad,
+                                  dv0 + (uint64_t)((st * S::kTile + c * BN * S::W + k * 32 * S::W) >> 4),
+                                  dp0 + (uint64_t)(((blk & 1) * S::kPBuf + k * 32 * 16) >> 4), idesc_pv, k > 0);
+      ptx::umma_commit_elect(&bars->pv_full[blk & 1]);
+      ptx::umma_commit_elect(&bars->v_empty[st]);
+      return true;
+    };
+    // Blocks of all segments in one chain: QK runs one block ahead of PV.  The
+    // S buffer of QK(b) was read before P(b - 2) was published, which PV(b - 2),
+    // issued earlier, waited for; the O and P buffers of PV(b) are free once
+    // P(b) is published (the softmax threads read PV(b - 2) before that).
+    int pending = -1;
+    while (ok && run.next()) {
+      const int last = run.last_block();
+      if (last == run.b0) continue;
+      ok = wait_warp(&bars->q_full[seg & 1], (uint32_t)((seg >> 1) & 1), abort_flag, a.err);
+      for (int b = run.b0; ok && b < last; ++b, ++gb) {
+        ok = qk(gb, seg & 1);
+        if (ok && b + 1 == last) ptx::umma_commit_elect(&bars->q_empty[seg & 1]);
+        if (ok && pending >= 0) ok = pv(pending);
+        pending = gb;
+      }
+      ++seg;
+    }
+    if (ok && pending >= 0) pv(pending);
+    ptx::umma_commit_elect(&bars->drain);
+    ptx::mbar_wait(&bars->drain, 0);
+    __syncwarp();
+  } else if (warp == 6) {
+    // ------------------------------------------------- the parts of Q
+    int seg = 0;
+    constexpr int E = D / 32;          // values per lane
+    const float f = a.scale * kLog2e;
+    while (run.next()) {
+      if (run.last_block() == run.b0) continue;
+      const int qb = seg & 1;
+      if (seg >= 2 && !wait_warp(&bars->q_empty[qb], (uint32_t)(((seg >> 1) & 1) ^ 1), abort_flag, a.err)) break;
+#pragma unroll 2
+      for (int r = 0; r < R; ++r) {
+        const int rho = run.grp * R + r;
+        const bool ok = rho < run.q_len * G;
+        float x[E];
+        uint32_t amax = 0;
+        const T *src = static_cast<const T *>(a.q) +
+                       ((size_t)(run.q0 + (ok ? rho / G : 0)) * a.hq + run.hk * G + (ok ? rho % G : 0)) * D + lane * E;
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+          for (int e = 0; e < E; e += 2) {
+            const float2 v = *reinterpret_cast<const float2 *>(src + e);
+            x[e] = v.x;
+            x[e + 1] = v.y;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; e += 2) {
+            const uint32_t v = *reinterpret_cast<const uint32_t *>(src + e);
+            x[e] = __uint_as_float(v << 16);
+            x[e + 1] = __uint_as_float(v & 0xffff0000u);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          if (!ok) x[e] = 0.f;
+          amax = max(amax, __float_as_uint(x[e]) & 0x7fffffffu);
+        }
+        amax = __reduce_max_sync(0xffffffffu, amax);
+        const uint32_t code = scale_code(amax);
+        const float inv = code == kScaleNan ? 0.f : inverse_scale(code);
+        // byte of part p, value d: row p * R + r of the K-major tile, 16-byte chunks swizzled
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = code == kScaleNan ? 0.f : x[e] * inv;
+        const int d0 = lane * E, c = d0 / S::W, dd = d0 % S::W;
+#pragma unroll
+        for (int p = 0; p < S::NQ; ++p) {
+          const int row = p * R + r;
+          const int sz = S::W == 128 ? row & 7 : (row >> 1) & 3;
+          uint8_t *dst = sQ + qb * S::kQBuf + c * S::NQpad * S::W + row * S::W + (((dd >> 4) ^ sz) << 4) + (dd & 15);
+#pragma unroll
+          for (int e = 0; e < E; e += 2) {
+            const uint32_t v = to_e4m3x2(x[e], x[e + 1]);
+            const float2 b = __half22float2(from_e4m3x2(v));
+            x[e] = (x[e] - b.x) * 16.f;
+            x[e + 1] = (x[e + 1] - b.y) * 16.f;
+            *reinterpret_cast<uint16_t *>(dst + e) = (uint16_t)v;
+          }
+        }
+        if (lane == 0) {
+          s_qf[qb * 16 + r] = scale_value(code) * f;
+          s_end[qb * 16 + r] = run.row_end(r);
+        }
+      }
+      ptx::fence_proxy_async_smem();
+      ptx::mbar_arrive(&bars->q_full[qb]);
+      ++seg;
+    }
+  } else if (warp == 7) {
+    // ------------------------------------------------------ the scales
+    int gb = 0;
+    bool ok = true;
+    while (ok && run.next()) {
+      const int last = run.last_block();
+      const int32_t *pt = a.page_table + (size_t)run.s * a.max_pages;
+      auto page_of = [&](int b) -> int {
+        const int pos = b * BN + lane * 4;
+        return b < last && pos < run.kv ? pt[pos >> a.p_shift] : -1;
+      };
+      int next_page = page_of(run.b0);
+      for (int b = run.b0; b < last; ++b, ++gb) {
+        const int page = next_page;
+        next_page = page_of(b + 1);
+        const int slot = gb % kScaleSlots;
+        if (gb >= kScaleSlots &&
+            !wait_warp(&bars->sc_empty[slot], (uint32_t)(((gb / kScaleSlots) & 1) ^ 1), abort_flag, a.err)) {
+          ok = false;
+          break;
+        }
+        const int pos = b * BN + lane * 4;
+        uint8_t *dst = sSc + slot * 2 * BN + lane * 4;
+        if (pos < run.kv && page >= 0 && page < a.num_pages) {
+          const size_t src = ((size_t)page * a.hkv + run.hk) * a.p + (pos & (a.p - 1));
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ptx::smem_u32(dst)), "l"(a.c.ks + src)
+                       : "memory");
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ptx::smem_u32(dst + BN)), "l"(a.c.vs + src)
+                       : "memory");
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                           ptx::smem_u32(&bars->sc_full[slot]))
+                       : "memory");
+        } else {
+          *reinterpret_cast<uint32_t *>(dst) = 0;
+          *reinterpret_cast<uint32_t *>(dst + BN) = 0;
+          ptx::mbar_arrive(&bars->sc_full[slot]);
+        }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else {
+    // -------------------------------------- softmax, weights, output
+    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    int gb = 0, seg = 0;
+    bool ok = true;
+    bool head_written = false;
+    while (ok && run.next()) {
+      const int last = run.last_block();
+      float m[R], l[R], o[S::CT][R];    // o is in units of exp2(m)
+      float F = 0.f;                    // 2^ev / 256 of the block whose O^T is pending
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+#pragma unroll
+        for (int c = 0; c < S::CT; ++c) o[c][r] = 0.f;
+      }
+      // joins block blk's product, in units of the maxima before `al` moved them, into o
+      auto take_pv = [&](int blk, const float (&al)[R]) -> bool {
+        if (!wait_warp(&bars->pv_full[blk & 1], (uint32_t)((blk >> 1) & 1), abort_flag, a.err)) return false;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < S::CT; ++c)
+#pragma unroll
+          for (int r0 = 0; r0 < R; r0 += S::RC) {
+            float sum[S::RC];
+            join_parts<S::NP, R, S::RC>(tO + lane_base + ((blk & 1) * S::CT + c) * S::NPpad + r0, sum);
+#pragma unroll
+            for (int r = 0; r < S::RC; ++r) o[c][r0 + r] = fmaf(sum[r], F, o[c][r0 + r]) * al[r0 + r];
+          }
+        ptx::tc_fence_before();
+        return true;
+      };
+      if (last > run.b0) {
+        if (!wait_warp(&bars->q_full[seg & 1], (uint32_t)((seg >> 1) & 1), abort_flag, a.err)) break;
+        const float *qf = s_qf + (seg & 1) * 16;
+        const int *ends = s_end + (seg & 1) * 16;
+        int all = run.kv;               // keys that every row of the group sees
+#pragma unroll
+        for (int r = 0; r < R; ++r) all = min(all, ends[r]);
+        for (int b = run.b0; b < last; ++b, ++gb) {
+          const int slot = gb % kScaleSlots;
+          const int par = gb & 1;
+          if (!wait_warp(&bars->sc_full[slot], (uint32_t)((gb / kScaleSlots) & 1), abort_flag, a.err)) {
+            ok = false;
+            break;
+          }
+          const int pos = b * BN + tid;
+          const bool key = pos < run.kv;
+          uint32_t kc = sSc[slot * 2 * BN + tid], vc = sSc[slot * 2 * BN + BN + tid];
+          ptx::mbar_arrive(&bars->sc_empty[slot]);
+          // NaN of either scale makes the score NaN for the rows that see the key
+          const float kf = scale_value(kc) + (vc == kScaleNan ? NAN : 0.f);
+          const int ev = key && vc != kScaleNan ? (int)vc : 0;
+          if (!wait_warp(&bars->s_full[par], (uint32_t)((gb >> 1) & 1), abort_flag, a.err)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          float x[R];
+#pragma unroll
+          for (int r0 = 0; r0 < R; r0 += S::RC) {
+            float sum[S::RC];
+            join_parts<S::NQ, R, S::RC>(tS + lane_base + par * S::NQpad + r0, sum);
+#pragma unroll
+            for (int r = 0; r < S::RC; ++r) x[r0 + r] = sum[r] * (qf[r0 + r] * kf);
+          }
+          if (b * BN + BN > all) {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+              if (pos >= ends[r]) x[r] = -INFINITY;
+          }
+          // maxima of the block: warp, then the four warps through shared memory
+          float *wm = s_max + par * 64;
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const float mx = warp_max(x[r]);
+            if (lane == 0) wm[warp * 16 + r] = mx;
+          }
+          const int evw = __reduce_max_sync(0xffffffffu, ev);
+          if (lane == 0) s_ev[par * 4 + warp] = evw;
+          if (lane == 0) ptx::mbar_arrive(&bars->x_full[par]);
+          if (!wait_warp(&bars->x_full[par], (uint32_t)((gb >> 1) & 1), abort_flag, a.err)) {
+            ok = false;
+            break;
+          }
+          const int evm = max(max(s_ev[par * 4], s_ev[par * 4 + 1]), max(s_ev[par * 4 + 2], s_ev[par * 4 + 3]));
+          // weight scale 2^(ev - evm) * 256, 0 below the normal range
+          const int we = 127 + 8 + ev - evm;
+          const float wf = we > 0 && key && vc != kScaleNan ? __uint_as_float((uint32_t)we << 23) : 0.f;
+          float w[R], al[R];
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const float mb = fmaxf(fmaxf(wm[r], wm[16 + r]), fmaxf(wm[32 + r], wm[48 + r]));
+            const float mn = fmaxf(m[r], mb);
+            al[r] = m[r] == mn ? 1.f : ptx::ex2(m[r] - mn);
+            m[r] = mn;
+            const float p = ptx::ex2(x[r] - joined(mn));
+            l[r] = l[r] * al[r] + p;
+            // a NaN score is a NaN weight; a zero weight stays zero whatever the scale
+            w[r] = p * wf + (p != p ? p : 0.f);
+          }
+          uint32_t pw[S::CP / 4];
+#pragma unroll
+          for (int p = 0; p < S::NP; ++p) {
+#pragma unroll
+            for (int r = 0; r < R; r += 4) {
+              const uint32_t lo = to_e4m3x2(w[r], w[r + 1]), hi = to_e4m3x2(w[r + 2], w[r + 3]);
+              pw[(p * R + r) / 4] = lo | (hi << 16);
+              if (p + 1 < S::NP) {
+                const float2 bl = __half22float2(from_e4m3x2(lo)), bh = __half22float2(from_e4m3x2(hi));
+                w[r] = (w[r] - bl.x) * 16.f;
+                w[r + 1] = (w[r + 1] - bl.y) * 16.f;
+                w[r + 2] = (w[r + 2] - bh.x) * 16.f;
+                w[r + 3] = (w[r + 3] - bh.y) * 16.f;
+              }
+            }
+          }
+          uint8_t *dst = sP + par * S::kPBuf + tid * 16;
+#pragma unroll
+          for (int i = 0; i < S::NPpad / 16; ++i) {
+            uint32_t q4[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) q4[j] = i * 4 + j < S::CP / 4 ? pw[i * 4 + j < S::CP / 4 ? i * 4 + j : 0] : 0u;
+            *reinterpret_cast<uint4 *>(dst + i * BN * 16) = make_uint4(q4[0], q4[1], q4[2], q4[3]);
+          }
+          // V rows without a key hold whatever the page or the slot held: zeros
+          if (b * BN + BN > run.kv) {
+            const int st = gb % NS;
+            if (!wait_warp(&bars->v_full[st], (uint32_t)((gb / NS) & 1), abort_flag, a.err)) {
+              ok = false;
+              break;
+            }
+            if (!key)
+#pragma unroll
+              for (int c = 0; c < S::CT; ++c)
+#pragma unroll
+                for (int q = 0; q < S::W / 16; ++q)
+                  *reinterpret_cast<uint4 *>(sV + st * S::kTile + c * BN * S::W + tid * S::W + q * 16) =
+                      make_uint4(0, 0, 0, 0);
+          }
+          ptx::fence_proxy_async_smem();
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(&bars->p_full[par]);
+          if (b > run.b0 && !take_pv(gb - 1, al)) {
+            ok = false;
+            break;
+          }
+          F = __uint_as_float(evm > 8 ? (uint32_t)(evm - 8) << 23 : 1u << (evm + 14));   // 2^(evm - 127 - 8)
+        }
+        float one[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) one[r] = 1.f;
+        if (!ok || !take_pv(gb - 1, one)) {
+          ok = false;
+          break;
+        }
+        ptx::mbar_arrive(&bars->q_empty[seg & 1]);
+        // row sums of the 128 keys' threads
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], off);
+          if (lane == 0) s_l[warp * 16 + r] = l[r];
+        }
+        if (lane == 0) ptx::mbar_arrive(&bars->l_full);
+        if (!wait_warp(&bars->l_full, (uint32_t)(seg & 1), abort_flag, a.err)) {
+          ok = false;
+          break;
+        }
+        ++seg;
+        // (s_l is written again only behind the next segment's first x_full)
+#pragma unroll
+        for (int r = 0; r < R; ++r) l[r] = (s_l[r] + s_l[16 + r]) + (s_l[32 + r] + s_l[48 + r]);
+      }
+      const bool whole = run.b0 == 0 && run.b1 == run.nb;
+      if (whole) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int rho = run.grp * R + r;
+          if (rho >= run.q_len * G) continue;
+          const size_t row = (size_t)(run.q0 + rho / G) * a.hq + run.hk * G + rho % G;
+          const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+#pragma unroll
+          for (int c = 0; c < S::CT; ++c)
+            if (D >= 128 || tid < D) store(static_cast<T *>(a.out) + row * D + c * 128 + tid, o[c][r] * inv);
+          if (tid == 0 && a.lse != nullptr)
+            a.lse[row] = l[r] == 0.f ? -INFINITY : (joined(m[r]) + log2f(l[r])) * kLn2;
+        }
+      } else {
+        // 2 * cta: the run begins inside the group; 2 * cta + 1: it begins with it
+        const size_t slot = 2 * (size_t)cta + (run.b0 > 0 ? 0 : 1);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+#pragma unroll
+          for (int c = 0; c < S::CT; ++c)
+            if (D >= 128 || tid < D) g.o[(slot * R + r) * D + c * 128 + tid] = o[c][r];
+          if (tid == 0) {
+            g.ml[(slot * R + r) * 2] = m[r];
+            g.ml[(slot * R + r) * 2 + 1] = l[r];
+          }
+        }
+      }
+      if (!head_written && tid == 0)
+        g.heads[cta] = PartHead{run.s, run.hk, run.grp, run.b0};
+      head_written = true;
+    }
+    if (!head_written && tid == 0) g.heads[cta].begin = 0;
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == 5) ptx::tmem_dealloc(tmem, S::kTmem);
+}
+
+// Joins the partial results of one group and row.  Block (i, r): the group
+// that CTA i's run begins inside, if CTA i is the first to do so; its parts are
+// slot 2 (i - 1) + 1 (or 2 (i - 1), never: that CTA began the group), then 2 j of every
+// following CTA that begins inside the same group.
+template <typename T, int D, int R>
+__global__ void __launch_bounds__(256) combine_kernel(const Args g) {
+  constexpr int L = D / 4, W = 256 / L;      // lanes along a row, parts in flight
+  __shared__ float s_o[W][D];
+  __shared__ float s_l[W];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int i = blockIdx.x, r = blockIdx.y, ctas = gridDim.x, tid = threadIdx.x;
+  const PartHead h = g.heads[i];
+  if (h.begin <= 0) return;
+  auto same = [&](const PartHead &p) { return p.begin > 0 && p.seq == h.seq && p.hk == h.hk && p.grp == h.grp; };
+  if (same(g.heads[i - 1])) return;
+  const AttendArgs &a = g.a;
+  const int G = a.hq / a.hkv;
+  const int q0 = a.len.cu[h.seq], q_len = a.len.cu[h.seq + 1] - q0;
+  const int rho = h.grp * R + r;
+  if (rho >= q_len * G) return;
+  int end = i + 1;
+  while (end < ctas && same(g.heads[end])) ++end;
+  const int parts = end - i + 1;
+  auto slot = [&](int k) { return ((size_t)(k == 0 ? 2 * (i - 1) + 1 : 2 * (i + k - 1))) * R + r; };
+  // the maximum of all parts, by every thread
+  float M = -INFINITY;
+  for (int k = tid & 31; k < parts; k += 32) M = fmaxf(M, g.ml[slot(k) * 2]);
+  M = warp_max(M);
+  const int li = tid % L, wi = tid / L;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+  for (int k = wi; k < parts; k += W) {
+    const float mk = g.ml[slot(k) * 2], lk = g.ml[slot(k) * 2 + 1];
+    if (lk == 0.f) continue;               // saw no key: nothing there
+    const float wt = mk == M ? 1.f : ptx::ex2(joined(mk) - joined(M));
+    const float4 v = *reinterpret_cast<const float4 *>(g.o + slot(k) * D + li * 4);
+    acc.x = fmaf(wt, v.x, acc.x);
+    acc.y = fmaf(wt, v.y, acc.y);
+    acc.z = fmaf(wt, v.z, acc.z);
+    acc.w = fmaf(wt, v.w, acc.w);
+    l = fmaf(wt, lk, l);
+  }
+  *reinterpret_cast<float4 *>(&s_o[wi][li * 4]) = acc;
+  if (li == 0) s_l[wi] = l;
+  __syncthreads();
+  if (tid < D) {
+    float v = 0.f, sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      v += s_o[w][tid];
+      sum += s_l[w];
+    }
+    const size_t row = (size_t)(q0 + rho / G) * a.hq + h.hk * G + rho % G;
+    store(static_cast<T *>(a.out) + row * D + tid, sum == 0.f ? 0.f : v / sum);
+    if (tid == 0 && a.lse != nullptr) a.lse[row] = sum == 0.f ? -INFINITY : (joined(M) + log2f(sum)) * kLn2;
+  }
+}
+
+template <typename T, int D, int R>
+cudaError_t launch_t(const AttendArgs &a, int q_limit, int grid, uint8_t *ws, cudaStream_t stream) {
+  using S = Shape<T, D, R>;
+  CUtensorMap tk, tv;
+  const uint64_t dims[3] = {(uint64_t)D, (uint64_t)a.hkv, (uint64_t)a.num_pages * a.p};
+  const uint64_t strides[2] = {(uint64_t)D, (uint64_t)a.hkv * D};
+  const uint32_t box[3] = {(uint32_t)S::W, 1, (uint32_t)(a.p < BN ? a.p : BN)};
+  if (!make_tmap_u8_3d(&tk, a.c.k, dims, strides, box) || !make_tmap_u8_3d(&tv, a.c.v, dims, strides, box))
+    return cudaErrorInvalidValue;
+  Args g{};
+  g.a = a;
+  g.q_limit = q_limit;
+  const RowsLayout w = rows_layout(grid, R, D);
+  g.heads = reinterpret_cast<PartHead *>(ws + w.heads);
+  g.ml = reinterpret_cast<float *>(ws + w.ml);
+  g.o = reinterpret_cast<float *>(ws + w.o);
+  auto kern = rows_kernel<T, D, R>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kThreads, S::kSmem, stream>>>(tk, tv, g);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || grid == 1) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3((unsigned)grid, R, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, combine_kernel<T, D, R>, g);
+}
+
+template <typename T, int D, int R> constexpr int ctas_of() { return Shape<T, D, R>::CTAS; }
+
+}  // namespace
+
+int rows_per_group(const rpa_dims &d, int32_t max_q) {
+  // the smallest group that holds a whole KV head's rows (its keys are then
+  // read once), up to 16; fp32 rows have three times the columns: up to 8
+  const int64_t rows = (int64_t)max_q * (d.num_q_heads / d.num_kv_heads);
+  if (rows <= 4) return 4;
+  if (rows <= 8 || d.dtype == RPA_F32) return 8;
+  return 16;
+}
+
+int rows_grid(const rpa_dims &d, int32_t max_seqs, int32_t max_q, int R) {
+  const int G = d.num_q_heads / d.num_kv_heads;
+  const int64_t cap = (int64_t)d.max_pages_per_seq * d.page_size;
+  const int64_t seqs = std::min<int64_t>(max_seqs, d.total_q_tokens);
+  const int64_t groups = ((int64_t)max_q * G + R - 1) / R;
+  int ctas = 1;
+  const bool f32 = d.dtype == RPA_F32;
+#define RPA_Q8_CTAS(DD)                                                                       \
+  case DD:                                                                                    \
+    ctas = f32 ? (R == 4 ? ctas_of<float, DD, 4>() : ctas_of<float, DD, 8>())                 \
+               : R == 4 ? ctas_of<__nv_bfloat16, DD, 4>()                                     \
+                        : R == 8 ? ctas_of<__nv_bfloat16, DD, 8>() : ctas_of<__nv_bfloat16, DD, 16>(); \
+    break;
+  switch (d.head_dim) {
+    RPA_Q8_CTAS(64)
+    RPA_Q8_CTAS(128)
+    RPA_Q8_CTAS(256)
+  }
+#undef RPA_Q8_CTAS
+  // one CTA per resident place on 148 SMs, fewer where the lengths cannot fill them
+  const double most = (double)seqs * groups * d.num_kv_heads * (double)((cap + BN - 1) / BN);
+  return (int)std::max(1.0, std::min(most, 148.0 * ctas));
+}
+
+RowsLayout rows_layout(int grid, int R, int D) {
+  RowsLayout w;
+  auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
+  w.heads = 0;
+  w.ml = up((int64_t)grid * sizeof(PartHead));
+  w.o = up(w.ml + (int64_t)grid * 2 * R * 2 * 4);
+  w.total = up(w.o + (int64_t)grid * 2 * R * D * 4);
+  return w;
+}
+
+cudaError_t launch_rows(const AttendArgs &a, const rpa_dims &d, int32_t max_seqs, int32_t max_q, int32_t q_limit,
+                        uint8_t *ws, cudaStream_t stream) {
+  const int R = rows_per_group(d, std::min(max_q, q_limit));
+  const int grid = rows_grid(d, max_seqs, std::min(max_q, q_limit), R);
+#define RPA_Q8_ROWS(DD)                                                                                   \
+  case DD:                                                                                                \
+    if (d.dtype == RPA_F32)                                                                               \
+      return R == 4 ? launch_t<float, DD, 4>(a, q_limit, grid, ws, stream)                                \
+                    : launch_t<float, DD, 8>(a, q_limit, grid, ws, stream);                               \
+    return R == 4   ? launch_t<__nv_bfloat16, DD, 4>(a, q_limit, grid, ws, stream)                        \
+           : R == 8 ? launch_t<__nv_bfloat16, DD, 8>(a, q_limit, grid, ws, stream)                        \
+                    : launch_t<__nv_bfloat16, DD, 16>(a, q_limit, grid, ws, stream);
+  switch (d.head_dim) {
+    RPA_Q8_ROWS(64)
+    RPA_Q8_ROWS(128)
+    RPA_Q8_ROWS(256)
+    default: return cudaErrorInvalidValue;
+  }
+#undef RPA_Q8_ROWS
+}
+
+}  // namespace q8
+}  // namespace rpa

@@ -72,6 +72,17 @@ class Q8Problem:
         val[bad] = 0.0
         return val
 
+    def v_scale(self, s, n, h):
+        """V scales of the n first cached rows of sequence s, head h (NaN and unreadable ones as 1)."""
+        pos = torch.arange(n)
+        page = self.table[s].long()[pos // self.p]
+        bad = (page < 0) | (page >= self.v_codes.shape[0])
+        e = scale_of(self.v_scales[torch.where(bad, 0, page), h, pos % self.p])
+        return torch.where(bad | torch.isnan(e), 1.0, e)
+
+    def v_top(self, s, n, h):
+        return self.v_scale(s, n, h).amax()
+
 
 def make(q_lens, kv_lens, *, hq, hkv, d, p, dtype=torch.bfloat16, causal=True, seed=0, spare=3, extra_width=1,
          poison=True, scale=None, gain=1.0):
@@ -117,6 +128,10 @@ def attend(pr: Q8Problem):
       the same: |out - ref| <= u |out| + A * (2 ds + w), w = 2 * 2^-8 for bf16
       and 2 * 2^-17 for fp32 (weights held to 17 bits or better there),
       plus 2^-16 A (2^-18 for fp32: a row's fp32 sums and exponentials);
+      and, whatever the weights, 2^-30 * 2^ev * sum_j |code_jd| / l over the visible keys, 2^ev the
+      largest V scale and l the softmax sum (its largest weight 1): a weight w, scaled so that
+      w 2^(ev_j - ev) 256 <= 256, is held as four e4m3 parts, each scaled by 16 against the one
+      before, so the last one's smallest step 2^-9 leaves 2^-10 / 16^3 / 256 = 2^-30;
       |lse - ref| <= ds + 2^-20 (1 + |lse|).
     """
     t = sum(pr.q_lens)
@@ -151,7 +166,10 @@ def attend(pr: Q8Problem):
                                  q[:, h].abs().amax(-1) * 2.0 ** -21 * kh.abs().sum(-1).amax())
                 out[at:at + a, h] = torch.where(nan[:, None], math.nan, o)
                 lse[at:at + a, h] = torch.where(nan, math.nan, l)
-                tol_o[at:at + a, h] = half * o.abs() + (pw @ vh.abs()) * (2 * ds[:, None] + w)
+                vmax = pr.v_top(s, b, h // g)
+                floor = 2.0 ** -30 * (seen.double() @ (vh.abs() / pr.v_scale(s, b, h // g)[:, None])) * vmax
+                tol_o[at:at + a, h] = (half * o.abs() + (pw @ vh.abs()) * (2 * ds[:, None] + w) +
+                                       floor / torch.where(some, total, 1.0)[:, None])
                 tol_l[at:at + a, h] = torch.where(some, ds + 2.0 ** -20 * (1 + l.abs()), 0.0)
         at += a
     return out, lse, tol_o, tol_l
