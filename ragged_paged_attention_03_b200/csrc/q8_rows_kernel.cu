@@ -25,10 +25,12 @@
 // O^T is read from TMEM into fp32 registers, which are rescaled when the
 // maximum moves: no read-modify-write of TMEM and no wait between blocks.
 //
-// Split of the work: the blocks of every (sequence, KV head, row group) in a
-// row are one list, cut into equal runs, one per CTA (every SM gets the same
-// number of blocks whatever the lengths).  A CTA computes its run from the
-// lengths in device memory, so there is no planning launch.  A run may begin and
+// Split of the work: the blocks of every (sequence, row group) of one KV head
+// in a row are one list, cut into equal runs, one per CTA (every SM gets the
+// same number of blocks whatever the lengths).  A CTA computes its run from the
+// lengths in device memory, so there is no planning launch.  The CTAs of all
+// heads with the same run are neighbours: they read the rows of a token, which lie
+// side by side, at about the same time.  A run may begin and
 // end inside a group: those partial results go to the workspace and
 // combine_kernel, queued behind with programmatic dependent launch, joins them
 // in the order of the keys (the same bits every time).
@@ -137,7 +139,7 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volati
 // sequence without keys has one, empty, so that its rows are written).
 struct SeqWork {
   int groups, nb;
-  __device__ __forceinline__ int64_t blocks(int hkv) const { return (int64_t)groups * hkv * nb; }
+  __device__ __forceinline__ int64_t blocks() const { return (int64_t)groups * nb; }
 };
 template <int R>
 __device__ __forceinline__ SeqWork seq_work(int q_len, int kv_len, int G, int q_limit) {
@@ -152,10 +154,10 @@ template <int R>
 struct Run {
   const AttendArgs *a;
   int n, G, q_limit;
-  int s, unit, blk;
+  int hk, s, grp_next, blk;
   int64_t left;
   // the current segment
-  int q0, q_len, kv, hk, grp, nb, b0, b1;
+  int q0, q_len, kv, grp, nb, b0, b1;
 
   __device__ __forceinline__ bool next() {
     if (left <= 0) return false;
@@ -166,19 +168,17 @@ struct Run {
       q_len = a->len.cu[s + 1] - q0;
       kv = a->len.kv[s];
       w = seq_work<R>(q_len, kv, G, q_limit);
-      if (unit < w.groups * a->hkv) break;
+      if (grp_next < w.groups) break;
       ++s;
-      unit = 0;
+      grp_next = 0;
     }
     nb = w.nb;
-    hk = unit / w.groups;
-    grp = unit - hk * w.groups;
+    grp = grp_next++;
     b0 = blk;
     const int take = (int)(left < nb - blk ? left : nb - blk);
     b1 = b0 + take;
     left -= take;
     blk = 0;
-    ++unit;
     return true;
   }
   // keys seen by row `row` of the group, and by its last row
@@ -248,19 +248,21 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
 
   const AttendArgs &a = g.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int cta = blockIdx.x, ctas = gridDim.x;
+  const int ctas = gridDim.x / a.hkv;           // of one head
+  const int hk = blockIdx.x % a.hkv, cta = blockIdx.x / a.hkv;
+  const int place = hk * ctas + cta;            // in the lists of partial results
   const int G = a.hq / a.hkv;
 
   // ---- this CTA's run of blocks
   const int n = checked_seqs(a.len);
   if (n < 0) {
-    if (cta == 0 && tid == 0) raise(a.err, RPA_DEV_BAD_LENGTHS);
-    if (tid == 0) g.heads[cta].begin = 0;
+    if (blockIdx.x == 0 && tid == 0) raise(a.err, RPA_DEV_BAD_LENGTHS);
+    if (tid == 0) g.heads[place].begin = 0;
     return;
   }
   int64_t mine = 0;
   for (int s = tid; s < n; s += kThreads)
-    mine += seq_work<R>(a.len.cu[s + 1] - a.len.cu[s], a.len.kv[s], G, g.q_limit).blocks(a.hkv);
+    mine += seq_work<R>(a.len.cu[s + 1] - a.len.cu[s], a.len.kv[s], G, g.q_limit).blocks();
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
   if (lane == 0) s_scan[warp] = mine;
@@ -273,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
   const int64_t first = per * cta + (cta < extra ? cta : extra);
   const int64_t count = per + (cta < extra ? 1 : 0);
   if (count == 0) {
-    if (tid == 0) g.heads[cta].begin = 0;
+    if (tid == 0) g.heads[place].begin = 0;
     return;
   }
   // the sequence holding block `first`: a scan over the sequences, 256 at a time
@@ -282,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
     const int s = s0 + tid;
     SeqWork w{0, 1};
     if (s < n) w = seq_work<R>(a.len.cu[s + 1] - a.len.cu[s], a.len.kv[s], G, g.q_limit);
-    const int64_t b = w.blocks(a.hkv);
+    const int64_t b = w.blocks();
     int64_t incl = b;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -357,7 +359,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
   run.G = G;
   run.q_limit = g.q_limit;
   run.s = (int)s_scan[8];
-  run.unit = (int)s_scan[9];
+  run.hk = hk;
+  run.grp_next = (int)s_scan[9];
   run.blk = (int)s_scan[10];
   run.left = count;
 
@@ -779,8 +782,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
             a.lse[row] = l[r] == 0.f ? -INFINITY : (joined(m[r]) + log2f(l[r])) * kLn2;
         }
       } else {
-        // 2 * cta: the run begins inside the group; 2 * cta + 1: it begins with it
-        const size_t slot = 2 * (size_t)cta + (run.b0 > 0 ? 0 : 1);
+        // 2 * place: the run begins inside the group; 2 * place + 1: it begins with it
+        const size_t slot = 2 * (size_t)place + (run.b0 > 0 ? 0 : 1);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
 #pragma unroll
@@ -793,10 +796,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
         }
       }
       if (!head_written && tid == 0)
-        g.heads[cta] = PartHead{run.s, run.hk, run.grp, run.b0};
+        g.heads[place] = PartHead{run.s, hk, run.grp, run.b0};
       head_written = true;
     }
-    if (!head_written && tid == 0) g.heads[cta].begin = 0;
+    if (!head_written && tid == 0) g.heads[place].begin = 0;
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -805,9 +808,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
 }
 
 // Joins the partial results of one group and row.  Block (i, r): the group
-// that CTA i's run begins inside, if CTA i is the first to do so; its parts are
-// slot 2 (i - 1) + 1 (or 2 (i - 1), never: that CTA began the group), then 2 j of every
-// following CTA that begins inside the same group.
+// that the run at place i begins inside, if it is the first to do so; its parts
+// are slot 2 (i - 1) + 1, where the run before began the group, then 2 j of i and
+// every following place whose run begins inside the same group.
 template <typename T, int D, int R>
 __global__ void __launch_bounds__(256) combine_kernel(const Args g) {
   constexpr int L = D / 4, W = 256 / L;      // lanes along a row, parts in flight
@@ -883,7 +886,7 @@ cudaError_t launch_t(const AttendArgs &a, int q_limit, int grid, uint8_t *ws, cu
   if (e != cudaSuccess) return e;
   kern<<<grid, kThreads, S::kSmem, stream>>>(tk, tv, g);
   e = cudaGetLastError();
-  if (e != cudaSuccess || grid == 1) return e;
+  if (e != cudaSuccess || grid == a.hkv) return e;   // one run per head: nothing is split
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = dim3((unsigned)grid, R, 1);
@@ -928,9 +931,11 @@ int rows_grid(const rpa_dims &d, int32_t max_seqs, int32_t max_q, int R) {
     RPA_Q8_CTAS(256)
   }
 #undef RPA_Q8_CTAS
-  // one CTA per resident place on 148 SMs, fewer where the lengths cannot fill them
-  const double most = (double)seqs * groups * d.num_kv_heads * (double)((cap + BN - 1) / BN);
-  return (int)std::max(1.0, std::min(most, 148.0 * ctas));
+  // the same number of CTAs for every head, as many as are resident on 148 SMs;
+  // fewer where the lengths cannot fill them
+  const double most = (double)seqs * groups * (double)((cap + BN - 1) / BN);
+  const int runs = std::max(1, 148 * ctas / d.num_kv_heads);
+  return d.num_kv_heads * (int)std::max(1.0, std::min(most, (double)runs));
 }
 
 RowsLayout rows_layout(int grid, int R, int D) {

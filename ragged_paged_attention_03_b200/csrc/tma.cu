@@ -54,7 +54,10 @@ bool make_tmap_u8_3d(CUtensorMap *map, const void *base, const uint64_t dims[3],
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), gdim, gstride, bx, es,
                   CU_TENSOR_MAP_INTERLEAVE_NONE,
                   box[0] == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                  // no wider than one row: the next bytes are another row's
+                  dims[0] >= 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                 : dims[0] >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 
