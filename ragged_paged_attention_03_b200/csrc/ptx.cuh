@@ -156,6 +156,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
+// Two fp32 -> packed f16x2 (round to nearest even); `lo` in the low half.
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // x rounded to bf16 (nearest even, as pack_bf16 does), as an fp32 value.
 __device__ __forceinline__ float round_bf16(float x) { return __uint_as_float(pack_bf16(x, 0.f) << 16); }
 
@@ -265,6 +272,13 @@ __host__ __device__ constexpr uint32_t umma_idesc_e4m3(int m, int n, bool a_mn, 
          | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16)
          | ((uint32_t)(n >> 3) << 17)   // N / 8
          | ((uint32_t)(m >> 4) << 24);  // M / 16
+}
+
+// Instruction descriptor of kind::f16 with fp16 A/B and fp32 accumulation.
+__host__ __device__ constexpr uint32_t umma_idesc_f16(int m, int n, bool b_mn_major) {
+  return (1u << 4)                      // D format: f32; A and B formats 0: f16
+         | ((b_mn_major ? 1u : 0u) << 16)
+         | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
 // Instruction descriptor of kind::f16 with bf16 A/B and fp32 accumulation.

@@ -14,19 +14,25 @@ namespace rpa {
 namespace q8 {
 namespace {
 
+// A sequence of at most this many rows per KV head (new tokens times G) reads its
+// keys once in the row-group kernel.
+constexpr int kRowsPerGroup = 16;
+
 struct AttendLayout {
-  int32_t q_limit;       // longest q_len of the row-group kernel
-  int64_t rows, total;   // byte offsets
+  int32_t q_limit;             // longest q_len of the row-group kernel; longer ones are the chunk kernel's
+  bool chunk;                  // the chunk kernel is launched too
+  int64_t rows, parts, total;  // byte offsets
 };
 
 AttendLayout attend_layout(const rpa_dims &d, int32_t max_seqs, int32_t max_q) {
   AttendLayout w{};
-  w.q_limit = INT32_MAX;
+  w.q_limit = chunk_takes(d) ? std::max(1, kRowsPerGroup / (d.num_q_heads / d.num_kv_heads)) : INT32_MAX;
+  w.chunk = max_q > w.q_limit;
   const int32_t q = std::min(max_q, w.q_limit);
   const int R = rows_per_group(d, q);
-  const RowsLayout r = rows_layout(rows_grid(d, max_seqs, q, R), R, d.head_dim);
   w.rows = 0;
-  w.total = r.total;
+  w.parts = w.total = rows_layout(rows_grid(d, max_seqs, q, R), R, d.head_dim).total;
+  if (w.chunk) w.total += chunk_layout(chunk_grid(d, max_seqs, max_q), d.head_dim).total;
   return w;
 }
 
@@ -94,6 +100,8 @@ extern "C" RPA_API int rpa_q8_attend(const void *q, const rpa_q8_cache *cache, c
   a.causal = causal ? 1 : 0;
   a.scale = scale;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
-  const cudaError_t e = launch_rows(a, *dims, max_seqs, max_q_len, w.q_limit, ws + w.rows, stream);
+  cudaError_t e = cudaSuccess;
+  if (w.chunk) e = launch_chunk(a, *dims, max_seqs, max_q_len, w.q_limit, ws + w.parts, stream);
+  if (e == cudaSuccess) e = launch_rows(a, *dims, max_seqs, max_q_len, w.q_limit, ws + w.rows, stream);
   return e == cudaSuccess ? RPA_OK : RPA_ERR_CUDA;
 }

@@ -1,0 +1,1107 @@
+// q8_chunk_kernel.cu -- attention over the 8-bit cache for chunks of query rows
+// (bf16, head_dim 64 / 128): bound by the tensor cores and the softmax.
+//
+// Mathematics.  The query rows of one KV head, row = token i * G + head g, are
+// the M side (a KV head's G query heads share every key tile); S = Q K^T and
+// O += P V are fp16 MMAs with fp32 accumulators and an online softmax in fp32
+// (log2 domain, lazily rescaled).  fp16 and not bf16: one instruction turns two
+// e4m3 codes into fp16 (64 a clock and SM measured, against 32 for the shifts and
+// masks that make bf16 of them), and P has 11 bits instead of 8.  Ranges are
+// kept by powers of two, which are exact:
+//   K tile:  code * 2^(ek - ekb), ekb the largest K scale of the 128 keys; the
+//            factor 2^ekb joins the row's score factor;
+//   V tile:  code * 2^(ev - evb) the same way; P of the block carries 2^(evb - evr)
+//            in its exponent, evr the row's own reference, moved (with a rescale of
+//            the row's O) when its contributions pass it by more than 2^6;
+//   both exact while the tile's scales lie within 2^15 of each other.  A "wide" tile,
+//            whose scales do not, holds the bare codes, and the softmax warps apply the
+//            scales in fp32, key by key, from global memory (slow, and rare: rows of
+//            one sequence that differ in size by more than 30,000 times);
+//   Q row:   q * 2^-eq, as the cache's rows are scaled, so every value is exact
+//            down to 2^-33 of the row's largest;
+//   P:       2^5 at the row's largest weight times V scale (up to 2^11 while the
+//            rescale is put off), so it has 11 bits down to 2^-19 of that and counts
+//            down to 2^-29.
+// A token whose K or V row is NaN gets a NaN key and a zero value: its column is
+// NaN for the rows that see it, and a masked column is dropped whatever it holds.
+//
+// Split of the work: as in the row-group kernel, the blocks of all items (two
+// 128-row tiles of one sequence and KV head) are one list, cut into equal runs,
+// one per CTA; runs that begin or end inside an item leave partial results that
+// combine_kernel joins.
+//
+// Roles (512 threads launched at 128 registers; setmaxnreg: 2 x 128 at 184 and
+// 2 x 128 at 72, together 65,536):
+//   warps 0-3, 4-7  softmax and output of tile 0 and 1 (one row per thread); they
+//                   also turn their tile's Q, landed by TMA as bf16, into scaled
+//                   fp16 in place
+//   warps 8-11      keys and values: code tiles, landed by TMA, into swizzled fp16 tiles
+//   warp 12         TMEM owner and MMA issue
+//   warp 13         walks the run: segment descriptors for the others, TMA of Q
+//   warp 14         TMA of the code tiles
+// TMEM (512 columns): S/P of tile 0 | S/P of tile 1 | O of tile 0 | O of tile 1.
+#include <cuda.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "ptx.cuh"
+#include "q8_common.cuh"
+#include "q8_kernels.h"
+#include "tma.h"
+
+namespace rpa {
+namespace q8 {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int BM = 128, BN = 128;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescale = 6.0f;    // lazy rescale of O: weights reach 2^(6 + kBase)
+constexpr int kBase = 5;
+constexpr int kWide = 15;           // a tile whose scales spread further is "wide"
+constexpr int kWideBit = 1 << 16;   // in the published ekb / evb
+constexpr int kExpSlots = 8;
+constexpr int kSegSlots = 8;
+
+template <int D>
+struct Shape {
+  static constexpr int NSK = D == 64 ? 4 : 2, NSV = NSK;   // fp16 tiles
+  static constexpr int NST = D == 64 ? 4 : 2;              // code tiles: K, V, K, V, ...
+  static constexpr int kHalves = D / 64;
+  static constexpr int kQBytes = kHalves * BM * 128;
+  static constexpr int kKVBytes = kHalves * BN * 128;
+  static constexpr int kCodes = BN * D;
+  static constexpr int kData = 2 * kQBytes + (NSK + NSV) * kKVBytes + NST * kCodes;
+  static constexpr int kSmem = 1024 + kData + 1536;
+  static constexpr uint32_t kTmemCols = 512, kColO = 256;
+};
+
+struct Bars {
+  uint64_t q_full[2], q_empty[2], qc_full[2];
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+  uint64_t c_full[4], c_empty[4];
+  uint64_t e_full[kExpSlots];
+  uint64_t s_full[2], p_full[2], p_half[2], pv_done[2], o_free[2];
+  uint64_t seg_full[kSegSlots], seg_empty[kSegSlots];
+  uint64_t drain;
+};
+
+// One item's part of the CTA's run, written by warp 13 for the others.
+struct Seg {
+  int32_t seq, hk, item, b0;
+  int32_t blocks;                // blocks to run; < 0: the end of the run
+  int32_t nt[2], rows[2];        // blocks and rows of each tile
+  int32_t q0, row0;              // first token of the sequence, of the item within it
+  int32_t kv, q_len;
+  int32_t whole;                 // the item begins and ends here
+  int32_t pad[2];
+};
+constexpr int kSegUsers = 1 + 1 + 4 + 8;   // warps that release a slot: MMA, TMA, converters, softmax
+
+struct PartHead {
+  int32_t seq, hk, item, begin;
+};
+
+struct Args {
+  AttendArgs a;
+  int32_t q_limit;       // sequences of at most this many new tokens are another kernel's
+  int32_t tpt;           // tokens per tile: 128 / G
+  PartHead *heads;       // [ctas]
+  float2 *ml;            // [2 * ctas][256] maximum (log2), sum
+  float4 *o;             // [2 * ctas][D / 4][256]
+};
+
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort_flag, uint32_t *err) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer();
+  while (!ptx::mbar_try_wait(bar, parity)) {
+    if (*abort_flag) return false;
+    if (ptx::globaltimer() - t0 > ptx::kWaitLimitNs) {
+      *abort_flag = 1;
+      raise(err, RPA_DEV_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort_flag, uint32_t *err) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, err));
+}
+
+// sum over i in [0, n) of floor((a i + b) / 128), a, b >= 0: by the quotients
+// and remainders of a and b, which leaves floor((a' i + b') / 128) with
+// a', b' < 128; its sum repeats every 128 terms.
+__device__ __forceinline__ int64_t floor_sum128(int64_t n, int64_t a, int64_t b) {
+  int64_t sum = (a >> 7) * (n * (n - 1) / 2) + (b >> 7) * n;
+  const int ar = (int)(a & 127), br = (int)(b & 127);
+  const int64_t turns = n >> 7;
+  const int rest = (int)(n & 127);
+  // i = 128 j + k: floor((ar i + br) / 128) = ar j + floor((ar k + br) / 128)
+  int64_t whole = 0, part = 0;
+  if (turns > 0)
+    for (int k = 0; k < 128; ++k) whole += (ar * k + br) >> 7;
+  for (int k = 0; k < rest; ++k) part += (ar * k + br) >> 7;
+  return sum + turns * whole + (int64_t)ar * 128 * (turns * (turns - 1) / 2) + part + (int64_t)ar * turns * rest;
+}
+
+// The items of one sequence and KV head.  Item i holds tokens [i TT, (i + 1) TT)
+// and sees the first end(i) keys; it has max(1, ceil(end / 128)) blocks.
+struct SeqItems {
+  int q_len, kv, TT, causal, items;
+  __device__ __forceinline__ int end_of(int tokens) const {   // keys that token `tokens - 1` sees
+    return causal ? min(kv, max(0, kv - q_len + tokens)) : kv;
+  }
+  __device__ __forceinline__ int blocks_of(int item) const {
+    return max(1, (end_of(min(q_len, (item + 1) * TT)) + BN - 1) / BN);
+  }
+  // blocks of items [0, n)
+  __device__ __forceinline__ int64_t before(int n) const {
+    if (n <= 0) return 0;
+    if (!causal) return (int64_t)n * max(1, (kv + BN - 1) / BN);
+    const int whole = min(n, q_len / TT);            // items with all their tokens
+    const int64_t c = (int64_t)kv - q_len;
+    // the first items whose last token sees no key have one block
+    const int64_t none = c >= 0 ? 0 : min((int64_t)whole, -c / TT);
+    int64_t sum = none;
+    if (whole > none) sum += floor_sum128(whole - none, TT, c + (none + 1) * TT + BN - 1);
+    if (n > whole) sum += blocks_of(n - 1);
+    return sum;
+  }
+};
+__device__ __forceinline__ SeqItems seq_items(int q_len, int kv, const Args &g) {
+  SeqItems w;
+  w.q_len = q_len;
+  w.kv = kv;
+  w.TT = 2 * g.tpt;
+  w.causal = g.a.causal;
+  w.items = q_len > g.q_limit ? (q_len + w.TT - 1) / w.TT : 0;
+  return w;
+}
+
+// The CTA's run of blocks, one segment per item it touches.
+struct Run {
+  const Args *g;
+  int n, s, hk, item, blk;
+  int64_t left;
+  SeqItems w;
+  int q0, row0, b0, b1, nb;      // of the current segment: first token of the item, its blocks
+  int nt[2];                     // blocks of the segment that tile t takes part in
+  int rows[2];                   // rows of tile t
+
+  __device__ __forceinline__ void load() {
+    q0 = g->a.len.cu[s];
+    w = seq_items(g->a.len.cu[s + 1] - q0, g->a.len.kv[s], *g);
+  }
+  __device__ __forceinline__ bool next() {
+    if (left <= 0) return false;
+    while (item >= w.items) {
+      item = 0;
+      if (w.items == 0 || ++hk >= g->a.hkv) {
+        hk = 0;
+        if (++s >= n) return false;
+        load();
+      }
+    }
+    row0 = item * w.TT;
+    nb = w.blocks_of(item);
+    b0 = blk;
+    b1 = b0 + (int)(left < nb - blk ? left : nb - blk);
+    left -= b1 - b0;
+    blk = 0;
+    ++item;
+    const int G = g->a.hq / g->a.hkv;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int tok = min(g->tpt, max(0, w.q_len - row0 - t * g->tpt));
+      rows[t] = tok * G;
+      const int vis = tok == 0 ? 0 : max(1, (w.end_of(row0 + t * g->tpt + tok) + BN - 1) / BN);
+      nt[t] = max(0, min(b1, vis) - b0);
+    }
+    return true;
+  }
+  __device__ __forceinline__ int blocks() const { return max(nt[0], nt[1]); }
+};
+
+template <int D>
+__device__ __forceinline__ void issue_qk(uint32_t tS, uint64_t dq, uint64_t dk) {
+  constexpr uint32_t idesc = ptx::umma_idesc_f16(128, BN, false);
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks) {
+    const uint32_t off = ((ks >> 2) * BM * 128 + (ks & 3) * 32) >> 4;
+    ptx::umma_ss_elect(tS, dq + off, dk + off, idesc, ks > 0 ? 1u : 0u);
+  }
+}
+
+// f16x2 with 2^(e - top) in both halves (0 below fp16's range), NaN if `nan`.
+__device__ __forceinline__ uint32_t half_factor(int e, int top, bool nan) {
+  const int d = e - top;
+  const uint32_t h = nan ? 0x7fffu : d >= -14 ? (uint32_t)(15 + d) << 10 : d >= -24 ? 1u << (24 + d) : 0u;
+  return h | (h << 16);
+}
+__device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t codes_h2(uint32_t v) {
+  const __half2 h = from_e4m3x2(v);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                 const __grid_constant__ CUtensorMap tm_v, const Args g) {
+  using S = Shape<D>;
+  constexpr int NSK = S::NSK, NSV = S::NSV;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *sQ = base;
+  uint8_t *sK = sQ + 2 * S::kQBytes;
+  uint8_t *sV = sK + NSK * S::kKVBytes;
+  uint8_t *sC = sV + NSV * S::kKVBytes;
+  Bars *bars = reinterpret_cast<Bars *>(base + S::kData);
+  int64_t *s_scan = reinterpret_cast<int64_t *>(bars + 1);       // [16 + 4]
+  int *s_exp = reinterpret_cast<int *>(s_scan + 20);             // [kExpSlots][2]
+  Seg *s_seg = reinterpret_cast<Seg *>(s_exp + 2 * kExpSlots);   // [kSegSlots]
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_seg + kSegSlots);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+  const AttendArgs &a = g.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cta = blockIdx.x, ctas = gridDim.x;
+  const int G = a.hq / a.hkv;
+  uint32_t *err = a.err;
+
+  // ---- this CTA's run of blocks
+  const int n = checked_seqs(a.len);
+  if (n < 0) {
+    if (cta == 0 && tid == 0) raise(err, RPA_DEV_BAD_LENGTHS);
+    if (tid == 0) g.heads[cta].begin = 0;
+    return;
+  }
+  int64_t mine = 0;
+  for (int s = tid; s < n; s += kThreads) {
+    const SeqItems w = seq_items(a.len.cu[s + 1] - a.len.cu[s], a.len.kv[s], g);
+    mine += w.before(w.items) * a.hkv;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) s_scan[warp] = mine;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) total += s_scan[w];
+  const int64_t per = total / ctas, extra = total - per * ctas;
+  const int64_t first = per * cta + (cta < extra ? cta : extra);
+  const int64_t count = per + (cta < extra ? 1 : 0);
+  if (count == 0) {
+    if (tid == 0) g.heads[cta].begin = 0;
+    return;
+  }
+  int64_t before = 0;
+  for (int s0 = 0; s0 < n; s0 += kThreads) {
+    const int s = s0 + tid;
+    SeqItems w{};
+    int64_t one = 0;
+    if (s < n) {
+      w = seq_items(a.len.cu[s + 1] - a.len.cu[s], a.len.kv[s], g);
+      one = w.before(w.items);
+    }
+    const int64_t b = one * a.hkv;
+    int64_t incl = b;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    __syncthreads();
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    int64_t excl = before + incl - b, round = 0;
+#pragma unroll
+    for (int w2 = 0; w2 < kThreads / 32; ++w2) {
+      if (w2 < warp) excl += s_scan[w2];
+      round += s_scan[w2];
+    }
+    if (first >= excl && first < excl + b) {
+      const int64_t off = first - excl;
+      const int hk = (int)(off / one);
+      const int64_t r = off - hk * one;
+      int lo = 0, hi = w.items - 1;          // the item: the largest with before(item) <= r
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (w.before(mid) <= r) lo = mid; else hi = mid - 1;
+      }
+      s_scan[16] = s;
+      s_scan[17] = hk;
+      s_scan[18] = lo;
+      s_scan[19] = r - w.before(lo);
+    }
+    before += round;
+    if (first < before) break;               // uniform
+  }
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&bars->q_full[i], 1);
+      ptx::mbar_init(&bars->q_empty[i], 1);
+      ptx::mbar_init(&bars->qc_full[i], 128);
+      ptx::mbar_init(&bars->s_full[i], 1);
+      ptx::mbar_init(&bars->p_full[i], 128);
+      ptx::mbar_init(&bars->p_half[i], 128);
+      ptx::mbar_init(&bars->pv_done[i], 1);
+      ptx::mbar_init(&bars->o_free[i], 128);
+    }
+    for (int i = 0; i < 4; ++i) {
+      ptx::mbar_init(&bars->k_full[i], 128);
+      ptx::mbar_init(&bars->k_empty[i], 1);
+      ptx::mbar_init(&bars->v_full[i], 128);
+      ptx::mbar_init(&bars->v_empty[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      ptx::mbar_init(&bars->c_full[i], 1);
+      ptx::mbar_init(&bars->c_empty[i], 128);
+    }
+    for (int i = 0; i < kExpSlots; ++i) ptx::mbar_init(&bars->e_full[i], 1);
+    for (int i = 0; i < kSegSlots; ++i) {
+      ptx::mbar_init(&bars->seg_full[i], 1);
+      ptx::mbar_init(&bars->seg_empty[i], kSegUsers);
+    }
+    ptx::mbar_init(&bars->drain, 1);
+    *abort_flag = 0;
+    ptx::fence_barrier_init();
+  }
+  if (warp == 12) {
+    ptx::tmem_alloc(tmem_slot, S::kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  if (tid == 13 * 32) ptx::tma_prefetch_desc(&tm_q);
+  if (tid == 14 * 32) {
+    ptx::tma_prefetch_desc(&tm_k);
+    ptx::tma_prefetch_desc(&tm_v);
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // the next segment of the run, or nullptr at its end (or after an abort)
+  int segs = 0;
+  auto next_seg = [&]() -> const Seg * {
+    const int slot = segs % kSegSlots;
+    if (!wait_warp(&bars->seg_full[slot], (uint32_t)((segs / kSegSlots) & 1), abort_flag, err)) return nullptr;
+    return s_seg[slot].blocks < 0 ? nullptr : &s_seg[slot];
+  };
+  auto done_seg = [&]() {
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&bars->seg_empty[segs % kSegSlots]);
+    ++segs;
+  };
+
+  if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
+    if (warp == 13) {
+      // ---------------------------------------------------------- TMA of Q
+      const uint64_t once = ptx::l2_evict_first_policy();
+      Run run;
+      run.g = &g;
+      run.n = n;
+      run.s = (int)s_scan[16];
+      run.hk = (int)s_scan[17];
+      run.item = (int)s_scan[18];
+      run.blk = (int)s_scan[19];
+      run.left = count;
+      run.load();
+      int uses[2] = {0, 0};
+      const uint32_t bytes = (uint32_t)(S::kHalves * 128 * g.tpt * G);
+      bool ok = true, more = true;
+      for (; ok && more; ++segs) {
+        const int slot = segs % kSegSlots;
+        if (segs >= kSegSlots)
+          ok = wait_warp(&bars->seg_empty[slot], (uint32_t)(((segs / kSegSlots) & 1) ^ 1), abort_flag, err);
+        if (!ok) break;
+        more = run.next();
+        if (lane == 0) {
+          Seg d{};
+          d.blocks = -1;
+          if (more)
+            d = Seg{run.s, run.hk, run.item - 1, run.b0, run.blocks(), {run.nt[0], run.nt[1]},
+                    {run.rows[0], run.rows[1]}, run.q0, run.row0, run.w.kv, run.w.q_len,
+                    run.b0 == 0 && run.b1 == run.nb ? 1 : 0, {0, 0}};
+          s_seg[slot] = d;
+          ptx::mbar_arrive(&bars->seg_full[slot]);
+        }
+        __syncwarp();
+        if (!more) break;
+        for (int t = 0; t < 2; ++t) {
+          const int nt = t ? run.nt[1] : run.nt[0];
+          if (!ok || nt == 0) continue;
+          const int u = t ? uses[1] : uses[0];
+          if (u > 0) ok = wait_warp(&bars->q_empty[t], (uint32_t)((u - 1) & 1), abort_flag, err);
+          if (!ok) continue;
+          ptx::mbar_arrive_expect_tx_elect(&bars->q_full[t], bytes);
+          for (int h = 0; h < S::kHalves; ++h)
+            ptx::tma_load_3d_hint_elect(sQ + t * S::kQBytes + h * BM * 128, &tm_q, &bars->q_full[t], h * 64,
+                                        run.hk * G, run.q0 + run.row0 + t * g.tpt, once);
+          if (t) ++uses[1]; else ++uses[0];
+        }
+      }
+      // queued copies land before the CTA ends
+      for (int t = 0; t < 2; ++t)
+        if (uses[t] > 0) ptx::mbar_wait(&bars->q_full[t], (uint32_t)((uses[t] - 1) & 1));
+      __syncwarp();
+    } else if (warp == 14) {
+      // ------------------------------------------------- TMA of the codes
+      const int br = a.p < BN ? a.p : BN;
+      const int nload = BN / br;
+      constexpr int W = D < 128 ? D : 128;
+      int use = 0;                       // code tiles queued
+      bool ok = true;
+      while (ok) {
+        const Seg *sg = next_seg();
+        if (sg == nullptr) break;
+        const int blocks = sg->blocks, b0 = sg->b0, kv = sg->kv, hk = sg->hk;
+        const int32_t *pt = a.page_table + (size_t)sg->seq * a.max_pages;
+        done_seg();
+        auto page_of = [&](int j) -> int {
+          const int pos = (b0 + j) * BN + lane * br;
+          return lane < nload && j < blocks && pos < kv ? pt[pos >> a.p_shift] : -1;
+        };
+        int next_page = page_of(0);
+        for (int j = 0; ok && j < blocks; ++j) {
+          const int page = next_page;
+          next_page = page_of(j + 1);
+          const int pos = (b0 + j) * BN + lane * br;
+          const bool load = lane < nload && pos < kv;
+          int row = page * a.p + (pos & (a.p - 1));
+          if (load && (page < 0 || page >= a.num_pages)) {
+            raise(err, RPA_DEV_BAD_PAGE);
+            row = a.num_pages * a.p;       // outside the tensor: the copy fills zeros
+          }
+          const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, load)) * (uint32_t)(br * D);
+#pragma unroll
+          for (int kv2 = 0; kv2 < 2; ++kv2, ++use) {
+            const int st = use % S::NST;
+            if (use >= S::NST &&
+                !wait_warp(&bars->c_empty[st], (uint32_t)(((use / S::NST) & 1) ^ 1), abort_flag, err)) {
+              ok = false;
+              break;
+            }
+            ptx::mbar_arrive_expect_tx_elect(&bars->c_full[st], bytes);
+            __syncwarp();
+            if (load)
+              ptx::tma_load_3d(sC + st * S::kCodes + lane * br * W, kv2 ? &tm_v : &tm_k, &bars->c_full[st], 0, hk, row);
+            __syncwarp();
+          }
+        }
+      }
+      // queued copies land before the CTA ends
+      if (lane == 0)
+        for (int k = use - S::NST < 0 ? 0 : use - S::NST; k < use; ++k)
+          ptx::mbar_wait(&bars->c_full[k % S::NST], (uint32_t)((k / S::NST) & 1));
+      __syncwarp();
+    } else if (warp == 12) {
+      // ---------------------------------------------------------------- MMA
+      // The tensor pipe sees, per segment, QK0(0) QK1(0) PV0(0) and then for every block j
+      // QK0(j+1) PV1(j) QK1(j+1) PV0(j+1): one tile's softmax runs beside the
+      // other's MMAs.  A QK into a tile's S/P columns follows the PV that reads P
+      // there; MMAs of one thread execute in order.
+      const uint64_t dq0 = ptx::umma_desc_sw128(ptx::smem_u32(sQ), 16, 1024);
+      const uint64_t dk0 = ptx::umma_desc_sw128(ptx::smem_u32(sK), 16, 1024);
+      const uint64_t dv0 = ptx::umma_desc_sw128(ptx::smem_u32(sV), BN * 128, 1024);
+      int gb = 0, gt0 = 0, gt1 = 0, ep0 = 0, ep1 = 0;
+      bool ok = true;
+      auto qk = [&](int t, int blk, bool wait) -> bool {
+        const int st = blk % NSK;
+        if (wait && !wait_warp(&bars->k_full[st], (uint32_t)((blk / NSK) & 1), abort_flag, err)) return false;
+        ptx::tc_fence_after();
+        issue_qk<D>(tmem + t * 128, dq0 + (uint64_t)((t * S::kQBytes) >> 4),
+                    dk0 + (uint64_t)((st * S::kKVBytes) >> 4));
+        ptx::umma_commit_elect(&bars->s_full[t]);
+        return true;
+      };
+      auto pv = [&](int t, int blk, int tblk, bool first, bool wait) -> bool {
+        constexpr uint32_t idesc = ptx::umma_idesc_f16(128, D, true);
+        const int st = blk % NSV;
+        const uint32_t tS = tmem + t * 128, tO = tmem + S::kColO + t * D;
+        if (!wait_warp(&bars->p_half[t], (uint32_t)(tblk & 1), abort_flag, err)) return false;
+        if (wait && !wait_warp(&bars->v_full[st], (uint32_t)((blk / NSV) & 1), abort_flag, err)) return false;
+        ptx::tc_fence_after();
+        const uint64_t dv = dv0 + (uint64_t)((st * S::kKVBytes) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < BN / 32; ++kk)
+          ptx::umma_ts_elect(tO, tS + kk * 8, dv + (uint64_t)((kk * 16 * 128) >> 4), idesc, (!first || kk > 0) ? 1u : 0u);
+        if (!wait_warp(&bars->p_full[t], (uint32_t)(tblk & 1), abort_flag, err)) return false;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int kk = BN / 32; kk < BN / 16; ++kk)
+          ptx::umma_ts_elect(tO, tS + kk * 8, dv + (uint64_t)((kk * 16 * 128) >> 4), idesc, 1u);
+        return true;
+      };
+      while (ok) {
+        const Seg *sg = next_seg();
+        if (sg == nullptr) break;
+        const int n0 = sg->nt[0], n1 = sg->nt[1], nb = sg->blocks;
+        done_seg();
+        if (nb == 0) continue;
+        if (n0 > 0) {
+          ok = wait_warp(&bars->qc_full[0], (uint32_t)(ep0 & 1), abort_flag, err) && qk(0, gb, true);
+          if (ok && n0 == 1) ptx::umma_commit_elect(&bars->q_empty[0]);
+        }
+        if (ok && n1 > 0) {
+          ok = wait_warp(&bars->qc_full[1], (uint32_t)(ep1 & 1), abort_flag, err) && qk(1, gb, n0 == 0);
+          if (ok && n1 == 1) ptx::umma_commit_elect(&bars->q_empty[1]);
+        }
+        if (ok) ptx::umma_commit_elect(&bars->k_empty[gb % NSK]);
+        if (ok && n0 > 0) {
+          if (ep0 > 0) ok = wait_warp(&bars->o_free[0], (uint32_t)((ep0 - 1) & 1), abort_flag, err);
+          ok = ok && pv(0, gb, gt0, true, true);
+          if (ok && n0 == 1) ptx::umma_commit_elect(&bars->pv_done[0]);
+        }
+        for (int j = 0; ok && j < nb; ++j) {
+          const bool k_waited = j + 1 < n0;
+          if (j + 1 < n0) {
+            ok = qk(0, gb + j + 1, true);
+            if (ok && j + 2 == n0) ptx::umma_commit_elect(&bars->q_empty[0]);
+          }
+          if (ok && j < n1) {
+            if (j == 0 && ep1 > 0) ok = wait_warp(&bars->o_free[1], (uint32_t)((ep1 - 1) & 1), abort_flag, err);
+            ok = ok && pv(1, gb + j, gt1 + j, j == 0, j >= n0);
+            if (ok && j + 1 == n1) ptx::umma_commit_elect(&bars->pv_done[1]);
+          }
+          if (ok) ptx::umma_commit_elect(&bars->v_empty[(gb + j) % NSV]);
+          if (ok && j + 1 < n1) {
+            ok = qk(1, gb + j + 1, !k_waited);
+            if (ok && j + 2 == n1) ptx::umma_commit_elect(&bars->q_empty[1]);
+          }
+          if (ok && j + 1 < nb) ptx::umma_commit_elect(&bars->k_empty[(gb + j + 1) % NSK]);
+          if (ok && j + 1 < n0) {
+            ok = pv(0, gb + j + 1, gt0 + j + 1, false, true);
+            if (ok && j + 2 == n0) ptx::umma_commit_elect(&bars->pv_done[0]);
+          }
+        }
+        gb += nb;
+        gt0 += n0;
+        gt1 += n1;
+        ep0 += n0 > 0 ? 1 : 0;
+        ep1 += n1 > 0 ? 1 : 0;
+      }
+      ptx::umma_commit_elect(&bars->drain);
+      ptx::mbar_wait(&bars->drain, 0);
+      __syncwarp();
+    }
+  } else if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
+    // ------------------------------------------------- keys and values
+    constexpr int LPR = D / 16;            // lanes of a row, 16 codes each
+    constexpr int RU = 32 / LPR;           // rows of one load instruction
+    constexpr int NU = BN / RU / 4;        // loads per thread and tile (4 warps)
+    const int cw = warp - 8;
+    const int lrow = lane / LPR, lcol = lane % LPR;
+    // one block ahead of time: which page and scales lane `lane`'s keys (4 lane .. + 3) have
+    struct Block {
+      const int32_t *pt;
+      int hk, kv, b;                       // b < 0: past the run
+    };
+    int seg_left = 0;
+    Block cursor{nullptr, 0, 0, -1};
+    auto advance = [&]() -> Block {
+      while (seg_left == 0) {
+        const Seg *sg = next_seg();
+        if (sg == nullptr) return Block{nullptr, 0, 0, -1};
+        seg_left = sg->blocks;
+        cursor = Block{a.page_table + (size_t)sg->seq * a.max_pages, sg->hk, sg->kv, sg->b0};
+        done_seg();
+      }
+      --seg_left;
+      const Block c = cursor;
+      ++cursor.b;
+      return c;
+    };
+    auto page_of = [&](const Block &c) -> int {
+      const int pos = c.b * BN + lane * 4;
+      if (c.b < 0 || pos >= c.kv) return -1;
+      const int pg = c.pt[pos >> a.p_shift];
+      if (pg >= 0 && pg < a.num_pages) return pg;
+      raise(err, RPA_DEV_BAD_PAGE);
+      return -1;
+    };
+    auto scales_of = [&](const Block &c, int pg, const uint8_t *src) -> uint32_t {
+      if (pg < 0) return 0;
+      const int pos = c.b * BN + lane * 4;
+      return *reinterpret_cast<const uint32_t *>(src + ((size_t)pg * a.hkv + c.hk) * a.p + (pos & (a.p - 1)));
+    };
+    // code tile -> fp16 tile; rows from `keys` on, which no copy filled, become zeros
+    auto convert = [&](uint8_t *dst, const uint8_t *src, uint32_t scales, uint32_t nans, int top, int keys,
+                       bool wide) {
+#pragma unroll
+      for (int i = 0; i < NU; ++i) {
+        const int row = (i * 4 + cw) * RU + lrow;
+        uint4 x = *reinterpret_cast<const uint4 *>(src + row * D + lcol * 16);
+        if (row >= keys) x = make_uint4(0, 0, 0, 0);
+        const int sh = (row & 3) * 8;
+        const int e = (int)((__shfl_sync(0xffffffffu, scales, row >> 2) >> sh) & 255u);
+        const bool nan = ((__shfl_sync(0xffffffffu, nans, row >> 2) >> sh) & 255u) != 0;
+        const uint32_t f = row < keys ? half_factor(wide ? top : e, top, nan) : 0u;
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        uint32_t h[8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          h[2 * q] = mul_h2(codes_h2(w[q] & 0xffffu), f);
+          h[2 * q + 1] = mul_h2(codes_h2(w[q] >> 16), f);
+        }
+        // values 16 lcol .. + 15: chunks 2 (lcol % 4), + 1 of column tile lcol / 4; lanes
+        // of odd column tiles store theirs in the other order (no bank is hit twice)
+        const int c0 = 2 * (lcol & 3), swp = (lcol >> 2) & 1;
+        uint8_t *p = dst + (lcol >> 2) * BN * 128 + row * 128;
+        const uint4 u0 = make_uint4(h[0], h[1], h[2], h[3]), u1 = make_uint4(h[4], h[5], h[6], h[7]);
+        *reinterpret_cast<uint4 *>(p + (((c0 + swp) ^ (row & 7)) << 4)) = swp ? u1 : u0;
+        *reinterpret_cast<uint4 *>(p + (((c0 + 1 - swp) ^ (row & 7)) << 4)) = swp ? u0 : u1;
+      }
+    };
+    Block cur = advance(), nxt = advance();
+    int pg = page_of(cur), pgn = page_of(nxt);
+    uint32_t ks = scales_of(cur, pg, a.c.ks), vs = scales_of(cur, pg, a.c.vs);
+    for (int gb = 0; cur.b >= 0; ++gb) {
+      const Block nn = advance();
+      const int pgnn = page_of(nn);
+      const uint32_t ksn = scales_of(nxt, pgn, a.c.ks), vsn = scales_of(nxt, pgn, a.c.vs);
+      // this block's largest scales over the keys it has; NaN scales mark the key
+      uint32_t nans = 0;
+      int ek = 0, ev = 0, ek0 = 255, ev0 = 255;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool key = pg >= 0 && cur.b * BN + lane * 4 + j < cur.kv;
+        const uint32_t k8 = (ks >> (8 * j)) & 255u, v8 = (vs >> (8 * j)) & 255u;
+        if (key && (k8 == kScaleNan || v8 == kScaleNan)) nans |= 255u << (8 * j);
+        if (key && k8 != kScaleNan) {
+          ek = max(ek, (int)k8);
+          ek0 = min(ek0, (int)k8);
+        }
+        if (key && v8 != kScaleNan) {
+          ev = max(ev, (int)v8);
+          ev0 = min(ev0, (int)v8);
+        }
+      }
+      ek = __reduce_max_sync(0xffffffffu, ek);
+      ev = __reduce_max_sync(0xffffffffu, ev);
+      const bool wk = ek - __reduce_min_sync(0xffffffffu, ek0) > kWide;
+      const bool wv = ev - __reduce_min_sync(0xffffffffu, ev0) > kWide;
+      const int sk = gb % NSK, sv = gb % NSV;
+      if (gb >= NSK && !wait_warp(&bars->k_empty[sk], (uint32_t)(((gb / NSK) & 1) ^ 1), abort_flag, err)) break;
+      if (warp == 8 && lane == 0) {
+        // free: QK of block gb - 4 or a later one is done for both tiles, and was issued
+        // behind the P of every block up to gb - 5
+        s_exp[(gb % kExpSlots) * 2] = ek | (wk ? kWideBit : 0);
+        s_exp[(gb % kExpSlots) * 2 + 1] = ev | (wv ? kWideBit : 0);
+        ptx::mbar_arrive(&bars->e_full[gb % kExpSlots]);
+      }
+      const int keys = cur.kv - cur.b * BN;
+      const int ck = 2 * gb % S::NST, cv = (2 * gb + 1) % S::NST;
+      if (!wait_warp(&bars->c_full[ck], (uint32_t)((2 * gb / S::NST) & 1), abort_flag, err)) break;
+      convert(sK + sk * S::kKVBytes, sC + ck * S::kCodes, ks, nans, ek, keys, wk);
+      ptx::fence_proxy_async_smem();
+      ptx::mbar_arrive(&bars->k_full[sk]);
+      ptx::mbar_arrive(&bars->c_empty[ck]);
+      if (gb >= NSV && !wait_warp(&bars->v_empty[sv], (uint32_t)(((gb / NSV) & 1) ^ 1), abort_flag, err)) break;
+      if (!wait_warp(&bars->c_full[cv], (uint32_t)(((2 * gb + 1) / S::NST) & 1), abort_flag, err)) break;
+      // the weight of a NaN key is NaN where it is seen; its codes are zeros, its scale 0 here
+      convert(sV + sv * S::kKVBytes, sC + cv * S::kCodes, vs & ~nans, 0u, ev, keys, wv);
+      ptx::fence_proxy_async_smem();
+      ptx::mbar_arrive(&bars->v_full[sv]);
+      ptx::mbar_arrive(&bars->c_empty[cv]);
+      cur = nxt;
+      nxt = nn;
+      pg = pgn;
+      pgn = pgnn;
+      ks = ksn;
+      vs = vsn;
+    }
+  } else {
+    // ------------------------------------------------------ softmax, output
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;" ::: "memory");
+    const int t = warp >> 2, row = tid & 127;
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t tS = lane_base + (uint32_t)(t * 128);
+    const uint32_t tO = lane_base + S::kColO + (uint32_t)(t * D);
+    const int tok = row / G, head = row - tok * G;
+    const float f = a.scale * kLog2e;
+    int gb = 0, gt = 0, ep = 0;
+    bool ok = true, head_written = false;
+    while (ok) {
+      const Seg *sg = next_seg();
+      if (sg == nullptr) break;
+      const int nt = sg->nt[t], nb = sg->blocks;
+      const bool mine = row < sg->rows[t];
+      const bool whole = sg->whole != 0;
+      const int b0 = sg->b0, hk = sg->hk;
+      const int32_t *pt = a.page_table + (size_t)sg->seq * a.max_pages;
+      const size_t slot = 2 * (size_t)cta + (b0 > 0 ? 0 : 1);
+      if (!head_written && tid == 0) g.heads[cta] = PartHead{sg->seq, sg->hk, sg->item, b0};
+      head_written = true;
+      const int tk = sg->row0 + t * g.tpt + tok;      // token within the sequence
+      const int end = !mine ? 0 : !a.causal ? sg->kv : min(sg->kv, max(0, sg->kv - sg->q_len + tk + 1));
+      const size_t at = (size_t)(sg->q0 + tk) * a.hq + sg->hk * G + head;   // the row in out and lse
+      done_seg();
+      if (nt == 0) {
+        // no block of this segment is seen by the tile: an empty part
+        if (!whole && mine) g.ml[slot * 256 + t * 128 + row] = make_float2(-INFINITY, 0.f);
+        gb += nb;
+        continue;
+      }
+      // ---- Q: bf16 as landed -> scaled fp16 in place (the row is this thread's)
+      if (!wait_warp(&bars->q_full[t], (uint32_t)(ep & 1), abort_flag, err)) {
+        ok = false;
+        break;
+      }
+      float qf;
+      {
+        uint8_t *q = sQ + t * S::kQBytes + row * 128;
+        uint32_t amax = 0;
+#pragma unroll
+        for (int h = 0; h < S::kHalves; ++h)
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(q + h * BM * 128 + ((c ^ (row & 7)) << 4));
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) amax = max(max(amax, (w[i] << 16) & 0x7fff0000u), w[i] & 0x7fff0000u);
+          }
+        const uint32_t code = scale_code(amax);
+        const float inv = code == kScaleNan ? 0.f : inverse_scale(code);
+        qf = scale_value(code) * f;
+#pragma unroll
+        for (int h = 0; h < S::kHalves; ++h)
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint4 *p = reinterpret_cast<uint4 *>(q + h * BM * 128 + ((c ^ (row & 7)) << 4));
+            const uint4 u = *p;
+            uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[i] = code == kScaleNan ? 0u : ptx::pack_f16(__uint_as_float(w[i] << 16) * inv,
+                                                            __uint_as_float(w[i] & 0xffff0000u) * inv);
+            *p = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        ptx::fence_proxy_async_smem();
+        ptx::mbar_arrive(&bars->qc_full[t]);
+      }
+      float m = -INFINITY, l = 0.f;                   // l counts 2^kBase per unit weight
+      int evr = 0;                                    // O is in units of 2^(m + evr - kBase)
+      for (int j = 0; j < nt; ++j) {
+        const int eslot = (gb + j) % kExpSlots;
+        if (!wait_warp(&bars->e_full[eslot], (uint32_t)(((gb + j) / kExpSlots) & 1), abort_flag, err) ||
+            !wait_warp(&bars->s_full[t], (uint32_t)((gt + j) & 1), abort_flag, err)) {
+          ok = false;
+          break;
+        }
+        const int ek = s_exp[eslot * 2] & 255, ev = s_exp[eslot * 2 + 1] & 255;
+        const bool wide_k = s_exp[eslot * 2] >= kWideBit, wide_v = s_exp[eslot * 2 + 1] >= kWideBit;
+        // scale byte of key i of a wide tile; -1: not seen, or its page is outside the pool
+        auto scale_byte = [&](const uint8_t *src, int i) -> int {
+          const int pos = (b0 + j) * BN + i;
+          const int pg = pos < end ? pt[pos >> a.p_shift] : -1;
+          if (pg < 0 || pg >= a.num_pages) return -1;
+          return src[((size_t)pg * a.hkv + hk) * a.p + (pos & (a.p - 1))];
+        };
+        ptx::tc_fence_after();
+        float x[BN];
+#pragma unroll
+        for (int cc = 0; cc < BN / 32; ++cc)
+          ptx::tmem_ld32(tS + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[cc * 32]));
+        ptx::tmem_ld_wait();
+        if (wide_k) {
+#pragma unroll
+          for (int i = 0; i < BN; ++i) {
+            const int d = scale_byte(a.c.ks, i) - ek;      // > 0: a NaN key, whose score is NaN already
+            x[i] *= d < -126 ? 0.f : __uint_as_float((uint32_t)(127 + min(d, 0)) << 23);
+          }
+        }
+        const int lim = min(BN, end - (b0 + j) * BN);
+        if (__any_sync(0xffffffffu, lim < BN)) {
+#pragma unroll
+          for (int i = 0; i < BN; ++i) x[i] = i < lim ? x[i] : -INFINITY;
+        }
+        float mq[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int i = 4; i < BN; i += 8) {
+          mq[0] = ptx::fmax3(mq[0], x[i], x[i + 1]);
+          mq[1] = ptx::fmax3(mq[1], x[i + 2], x[i + 3]);
+          if (i + 4 < BN) {
+            mq[2] = ptx::fmax3(mq[2], x[i + 4], x[i + 5]);
+            mq[3] = ptx::fmax3(mq[3], x[i + 6], x[i + 7]);
+          }
+        }
+        // never 0, which would make NaN of a masked score
+        float sc = qf * scale_value((uint32_t)ek);
+        if (sc < 1e-37f) sc = 1e-37f;
+        const float mx = ptx::fmax3(mq[0], mq[1], fmaxf(mq[2], mq[3])) * sc;
+        // the block's largest contribution, relative to 2^ev
+        float my = mx;
+        if (wide_v) {
+          my = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < BN; ++i) my = fmaxf(my, fmaf(x[i], sc, (float)(scale_byte(a.c.vs, i) - ev)));
+        }
+        const float m_new = fmaxf(m, mx);
+        // contributions of the row may pass the units of O by 2^kRescale
+        const bool need = m_new > m + kRescale || my + (float)(ev - evr) > m + kRescale;
+        if (__any_sync(0xffffffffu, need)) {
+          // PV(t, j - 1) is complete: s_full(t, j) was committed after QK(t, j), issued behind it.
+          // The new units: the larger of the old ones and the block's largest contribution
+          // (a row that has seen nothing has no old ones)
+          const float top = m == -INFINITY ? my + (float)ev : fmaxf(m + (float)evr, my + (float)ev);
+          const int evn = m_new == -INFINITY || top == -INFINITY ? evr : (int)ceilf(fmaxf(top - m_new, -300.f));
+          const float am = m == -INFINITY ? 0.f : ptx::ex2(m - m_new);
+          const float alpha = m == -INFINITY ? 0.f : ptx::ex2((m - m_new) + (float)(evr - evn));
+          if (j > 0) {
+#pragma unroll 1
+            for (int cc = 0; cc < D / 32; ++cc) {
+              uint32_t r[32];
+              ptx::tmem_ld32(tO + cc * 32, r);
+              ptx::tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+              ptx::tmem_st32(tO + cc * 32, r);
+            }
+          }
+          l *= am;
+          m = m_new;
+          evr = evn;
+        }
+        // values more than 2^64 below the row's units count as that small (the sum
+        // needs the weights above fp32's underflow)
+        const int dv = max(ev - evr, -64);
+        float shift = (m == -INFINITY ? 0.f : -m) + (float)(kBase + dv);
+        float wide_sum = 0.f;
+        if (wide_v) {
+          // the sum of the bare weights here, and x the exponents with the V scales
+          shift -= (float)dv;
+#pragma unroll
+          for (int i = 0; i < BN; ++i) {
+            const float y = fmaf(x[i], sc, shift);
+            wide_sum += ptx::ex2(y);
+            x[i] = y + (float)(scale_byte(a.c.vs, i) - evr);
+          }
+          sc = 1.f;
+          shift = 0.f;
+        }
+        const uint64_t scale2 = ptx::f2_pack(sc, sc);
+        const uint64_t shift2 = ptx::f2_pack(shift, shift);
+        uint64_t sp2[4] = {0, 0, 0, 0};
+        uint32_t pk[BN / 2];
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+          for (int i = hf * (BN / 2); i < (hf + 1) * (BN / 2); i += 2) {
+            float a0, a1;
+            ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(x[i], x[i + 1]), scale2, shift2), a0, a1);
+            float p0 = ptx::ex2(a0), p1 = ptx::ex2(a1);
+            sp2[(i >> 1) & 3] = ptx::f2_add(sp2[(i >> 1) & 3], ptx::f2_pack(p0, p1));
+            pk[i >> 1] = ptx::pack_f16(p0, p1);
+          }
+          ptx::tmem_st32(tS + hf * 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[hf * 32]));
+          if (hf == 0) {
+            ptx::tmem_st_wait();
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(&bars->p_half[t]);
+          }
+        }
+        float sp[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ptx::f2_unpack(sp2[k], sp[2 * k], sp[2 * k + 1]);
+        const float sum = ((sp[0] + sp[1]) + (sp[2] + sp[3])) + ((sp[4] + sp[5]) + (sp[6] + sp[7]));
+        // weights of this block carry 2^dv
+        l += wide_v ? wide_sum : sum * ptx::ex2((float)-dv);
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(&bars->p_full[t]);
+      }
+      if (!ok) break;
+      gb += nb;
+      gt += nt;
+      if (!wait_warp(&bars->pv_done[t], (uint32_t)(ep & 1), abort_flag, err)) {
+        ok = false;
+        break;
+      }
+      ptx::tc_fence_after();
+      uint32_t ov[D];
+#pragma unroll
+      for (int cc = 0; cc < D / 32; ++cc)
+        ptx::tmem_ld32(tO + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&ov[cc * 32]));
+      ptx::tmem_ld_wait();
+      ptx::tc_fence_before();
+      ptx::mbar_arrive(&bars->o_free[t]);
+      ++ep;
+      const float unit = ptx::ex2((float)(evr - 127));  // O / l is in units of this
+      if (end == 0) {                                 // sees no key, whatever its q holds
+        l = 0.f;
+        m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < D; ++i) ov[i] = 0;
+      }
+      if (mine) {
+        if (whole) {
+          const float inv = l == 0.f ? 0.f : unit / l;
+          __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + at * D;
+          const uint64_t once = ptx::l2_evict_first_policy();
+#pragma unroll
+          for (int cc = 0; cc < D / 8; ++cc) {
+            uint32_t o2[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              o2[i] = ptx::pack_bf16(__uint_as_float(ov[cc * 8 + 2 * i]) * inv,
+                                     __uint_as_float(ov[cc * 8 + 2 * i + 1]) * inv);
+            ptx::st_global_hint(reinterpret_cast<uint4 *>(out) + cc, make_uint4(o2[0], o2[1], o2[2], o2[3]), once);
+          }
+          if (a.lse != nullptr)
+            a.lse[at] = l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l) - kBase) * kLn2;
+        } else {
+          g.ml[slot * 256 + t * 128 + row] = make_float2(m, l);
+          float4 *po = g.o + slot * (D / 4) * 256 + t * 128 + row;
+#pragma unroll
+          for (int cc = 0; cc < D / 4; ++cc)
+            po[cc * 256] = make_float4(__uint_as_float(ov[cc * 4]) * unit, __uint_as_float(ov[cc * 4 + 1]) * unit,
+                                       __uint_as_float(ov[cc * 4 + 2]) * unit, __uint_as_float(ov[cc * 4 + 3]) * unit);
+        }
+      }
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == 12) ptx::tmem_dealloc(tmem, S::kTmemCols);
+}
+
+// Joins the parts of an item that several runs share (see the row-group
+// kernel's): block (i, y) joins 32 of the item's 256 rows.
+template <int D>
+__global__ void __launch_bounds__(256) combine_kernel(const Args g) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int i = blockIdx.x, ctas = gridDim.x;
+  const PartHead h = g.heads[i];
+  if (h.begin <= 0) return;
+  auto same = [&](const PartHead &p) { return p.begin > 0 && p.seq == h.seq && p.hk == h.hk && p.item == h.item; };
+  if (same(g.heads[i - 1])) return;
+  const AttendArgs &a = g.a;
+  const int G = a.hq / a.hkv;
+  const int q0 = a.len.cu[h.seq], q_len = a.len.cu[h.seq + 1] - q0;
+  const int r = blockIdx.y * 32 + (threadIdx.x & 31), t = r >> 7, row = r & 127;
+  const int tok = row / G, tk = (2 * h.item + t) * g.tpt + tok;
+  if (tok >= g.tpt || tk >= q_len) return;
+  int end = i + 1;
+  while (end < ctas && same(g.heads[end])) ++end;
+  const int parts = end - i + 1;
+  auto slot = [&](int k) { return (size_t)(k == 0 ? 2 * (i - 1) + 1 : 2 * (i + k - 1)); };
+  float M = -INFINITY, l = 0.f;
+  for (int k = 0; k < parts; ++k) M = fmaxf(M, g.ml[slot(k) * 256 + r].x);
+  constexpr int NC = D / 32;                 // float4 pieces per thread: 8 threads share a row
+  const int c0 = threadIdx.x >> 5;
+  float4 acc[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = 0; k < parts; ++k) {
+    const float2 ml = g.ml[slot(k) * 256 + r];
+    if (ml.y == 0.f) continue;               // saw no key: nothing there
+    const float wt = ml.x == M ? 1.f : ptx::ex2((ml.x == -INFINITY ? 0.f : ml.x) - (M == -INFINITY ? 0.f : M));
+    l = fmaf(wt, ml.y, l);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const float4 v = g.o[(slot(k) * (D / 4) + c * 8 + c0) * 256 + r];
+      acc[c].x = fmaf(wt, v.x, acc[c].x);
+      acc[c].y = fmaf(wt, v.y, acc[c].y);
+      acc[c].z = fmaf(wt, v.z, acc[c].z);
+      acc[c].w = fmaf(wt, v.w, acc[c].w);
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const size_t at = (size_t)(q0 + tk) * a.hq + h.hk * G + row % G;
+  __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + at * D;
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+    *reinterpret_cast<uint2 *>(out + (c * 8 + c0) * 4) =
+        make_uint2(ptx::pack_bf16(acc[c].x * inv, acc[c].y * inv), ptx::pack_bf16(acc[c].z * inv, acc[c].w * inv));
+  if (c0 == 0 && a.lse != nullptr)
+    a.lse[at] = l == 0.f ? -INFINITY : ((M == -INFINITY ? 0.f : M) + log2f(l) - kBase) * kLn2;
+}
+
+template <int D>
+cudaError_t launch_t(const AttendArgs &a, int q_limit, int total_q, int grid, uint8_t *ws, cudaStream_t stream) {
+  using S = Shape<D>;
+  Args g{};
+  g.a = a;
+  g.q_limit = q_limit;
+  const int G = a.hq / a.hkv;
+  g.tpt = BM / G;
+  const ChunkLayout w = chunk_layout(grid, D);
+  g.heads = reinterpret_cast<PartHead *>(ws + w.heads);
+  g.ml = reinterpret_cast<float2 *>(ws + w.ml);
+  g.o = reinterpret_cast<float4 *>(ws + w.o);
+  CUtensorMap tk, tv;
+  const uint64_t cdims[3] = {(uint64_t)D, (uint64_t)a.hkv, (uint64_t)a.num_pages * a.p};
+  const uint64_t cstrides[2] = {(uint64_t)D, (uint64_t)a.hkv * D};
+  const uint32_t cbox[3] = {(uint32_t)D, 1, (uint32_t)(a.p < BN ? a.p : BN)};
+  if (!make_tmap_u8_3d(&tk, a.c.k, cdims, cstrides, cbox, false) ||
+      !make_tmap_u8_3d(&tv, a.c.v, cdims, cstrides, cbox, false))
+    return cudaErrorInvalidValue;
+  // a tile of Q: the G heads of tpt tokens, token-major
+  CUtensorMap tq;
+  const uint64_t dims[3] = {(uint64_t)D, (uint64_t)a.hq, (uint64_t)total_q};
+  const uint64_t strides[2] = {(uint64_t)D * 2, (uint64_t)a.hq * D * 2};
+  const uint32_t box[3] = {64, (uint32_t)G, (uint32_t)g.tpt};
+  if (!make_tmap_bf16_3d(&tq, a.q, dims, strides, box, true)) return cudaErrorInvalidValue;
+  auto kern = chunk_kernel<D>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kThreads, S::kSmem, stream>>>(tq, tk, tv, g);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || grid == 1) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3((unsigned)grid, 8, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, combine_kernel<D>, g);
+}
+
+}  // namespace
+
+bool chunk_takes(const rpa_dims &d) { return d.dtype == RPA_BF16 && d.head_dim <= 128; }
+
+int chunk_grid(const rpa_dims &d, int32_t max_seqs, int32_t max_q) {
+  const int64_t cap = (int64_t)d.max_pages_per_seq * d.page_size;
+  const int TT = 2 * (BM / (d.num_q_heads / d.num_kv_heads));
+  const int64_t seqs = std::min<int64_t>(max_seqs, d.total_q_tokens);
+  const double most = (double)seqs * d.num_kv_heads * (double)((max_q + TT - 1) / TT) * (double)((cap + BN - 1) / BN);
+  return (int)std::max(1.0, std::min(most, 148.0));
+}
+
+ChunkLayout chunk_layout(int grid, int D) {
+  ChunkLayout w;
+  auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
+  w.heads = 0;
+  w.ml = up((int64_t)grid * sizeof(PartHead));
+  w.o = up(w.ml + (int64_t)grid * 2 * 256 * 8);
+  w.total = up(w.o + (int64_t)grid * 2 * 256 * D * 4);
+  return w;
+}
+
+cudaError_t launch_chunk(const AttendArgs &a, const rpa_dims &d, int32_t max_seqs, int32_t max_q, int32_t q_limit,
+                         uint8_t *ws, cudaStream_t stream) {
+  const int grid = chunk_grid(d, max_seqs, max_q);
+  switch (d.head_dim) {
+    case 64: return launch_t<64>(a, q_limit, d.total_q_tokens, grid, ws, stream);
+    case 128: return launch_t<128>(a, q_limit, d.total_q_tokens, grid, ws, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace q8
+}  // namespace rpa

@@ -13,14 +13,16 @@
 // each part takes 4 bits of the significand, and the remainder of a rounding is
 // exact in fp32, so
 //   bf16 I/O: 2 parts of Q (exact down to 2^-21 of the row's largest |q|),
-//             4 of P (16 bits; weights down to 2^-30 of the largest count, so a
-//             long flat tail behind one large weight keeps its sum);
+//             4 of P (16 bits; weights down to 2^-30 of the row's largest count,
+//             so a long flat tail behind one large weight keeps its sum);
 //   fp32 I/O: 6 parts of both (24 bits, as the fp32 values they come from).
 // The parts are columns of the same MMA (N = parts * R, whose time below
 // N = 64 is that of reading A), and their products are joined in fp32.
 // Scales: a key's K scale multiplies its score and its V scale its weight; one
-// thread owns one key, so both are a scalar of that thread.  Weights are scaled
-// by 2^(ev - max ev of the block) * 256 before the rounding to parts.
+// thread owns one key, so both are a scalar of that thread.  A weight with its V
+// scale, exp2(x + ev), is taken relative to the largest of its row and block
+// (times 256) before the rounding to parts: keys that a row does not see, or whose
+// weight is small, do not coarsen it however large their values are.
 // Softmax: running maximum and sum in fp32 (log2 domain).  Each block's product
 // O^T is read from TMEM into fp32 registers, which are rescaled when the
 // maximum moves: no read-modify-write of TMEM and no wait between blocks.
@@ -239,9 +241,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
   Bars *bars = reinterpret_cast<Bars *>(sSc + kScaleSlots * 2 * BN);
   float *s_qf = reinterpret_cast<float *>(bars + 1);       // [2][16] row factors
   int *s_end = reinterpret_cast<int *>(s_qf + 32);         // [2][16] keys each row sees
-  float *s_max = reinterpret_cast<float *>(s_end + 32);    // [2][4][16] warps' maxima
-  int *s_ev = reinterpret_cast<int *>(s_max + 128);        // [2][4] warps' largest V scale
-  float *s_l = reinterpret_cast<float *>(s_ev + 8);        // [4][16]
+  float *s_max = reinterpret_cast<float *>(s_end + 32);    // [2][4][16 + 16] warps' maxima of x, x + ev
+  float *s_l = reinterpret_cast<float *>(s_max + 256);       // [4][16]
   int64_t *s_scan = reinterpret_cast<int64_t *>(s_l + 64); // [8 + 3]
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_scan + 12);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -601,11 +602,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
     while (ok && run.next()) {
       const int last = run.last_block();
       float m[R], l[R], o[S::CT][R];    // o is in units of exp2(m)
-      float F = 0.f;                    // 2^ev / 256 of the block whose O^T is pending
+      float F[R];                       // what the pending block's O^T counts in units of exp2(m)
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         m[r] = -INFINITY;
-        l[r] = 0.f;
+        l[r] = F[r] = 0.f;
 #pragma unroll
         for (int c = 0; c < S::CT; ++c) o[c][r] = 0.f;
       }
@@ -620,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
             float sum[S::RC];
             join_parts<S::NP, R, S::RC>(tO + lane_base + ((blk & 1) * S::CT + c) * S::NPpad + r0, sum);
 #pragma unroll
-            for (int r = 0; r < S::RC; ++r) o[c][r0 + r] = fmaf(sum[r], F, o[c][r0 + r]) * al[r0 + r];
+            for (int r = 0; r < S::RC; ++r) o[c][r0 + r] = fmaf(sum[r], F[r0 + r], o[c][r0 + r]) * al[r0 + r];
           }
         ptx::tc_fence_before();
         return true;
@@ -645,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
           ptx::mbar_arrive(&bars->sc_empty[slot]);
           // NaN of either scale makes the score NaN for the rows that see the key
           const float kf = scale_value(kc) + (vc == kScaleNan ? NAN : 0.f);
-          const int ev = key && vc != kScaleNan ? (int)vc : 0;
+          const float ev = key && vc != kScaleNan ? (float)((int)vc - 127) : 0.f;
           if (!wait_warp(&bars->s_full[par], (uint32_t)((gb >> 1) & 1), abort_flag, a.err)) {
             ok = false;
             break;
@@ -665,34 +666,31 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
               if (pos >= ends[r]) x[r] = -INFINITY;
           }
           // maxima of the block: warp, then the four warps through shared memory
-          float *wm = s_max + par * 64;
+          float *wm = s_max + par * 128;
 #pragma unroll
           for (int r = 0; r < R; ++r) {
-            const float mx = warp_max(x[r]);
-            if (lane == 0) wm[warp * 16 + r] = mx;
+            const float mx = warp_max(x[r]), my = warp_max(x[r] + ev);
+            if (lane == 0) {
+              wm[warp * 32 + r] = mx;
+              wm[warp * 32 + 16 + r] = my;
+            }
           }
-          const int evw = __reduce_max_sync(0xffffffffu, ev);
-          if (lane == 0) s_ev[par * 4 + warp] = evw;
           if (lane == 0) ptx::mbar_arrive(&bars->x_full[par]);
           if (!wait_warp(&bars->x_full[par], (uint32_t)((gb >> 1) & 1), abort_flag, a.err)) {
             ok = false;
             break;
           }
-          const int evm = max(max(s_ev[par * 4], s_ev[par * 4 + 1]), max(s_ev[par * 4 + 2], s_ev[par * 4 + 3]));
-          // weight scale 2^(ev - evm) * 256, 0 below the normal range
-          const int we = 127 + 8 + ev - evm;
-          const float wf = we > 0 && key && vc != kScaleNan ? __uint_as_float((uint32_t)we << 23) : 0.f;
-          float w[R], al[R];
+          float w[R], al[R], Fn[R];
 #pragma unroll
           for (int r = 0; r < R; ++r) {
-            const float mb = fmaxf(fmaxf(wm[r], wm[16 + r]), fmaxf(wm[32 + r], wm[48 + r]));
+            const float mb = fmaxf(fmaxf(wm[r], wm[32 + r]), fmaxf(wm[64 + r], wm[96 + r]));
+            const float yb = joined(fmaxf(fmaxf(wm[16 + r], wm[48 + r]), fmaxf(wm[80 + r], wm[112 + r])));
             const float mn = fmaxf(m[r], mb);
             al[r] = m[r] == mn ? 1.f : ptx::ex2(m[r] - mn);
             m[r] = mn;
-            const float p = ptx::ex2(x[r] - joined(mn));
-            l[r] = l[r] * al[r] + p;
-            // a NaN score is a NaN weight; a zero weight stays zero whatever the scale
-            w[r] = p * wf + (p != p ? p : 0.f);
+            l[r] = l[r] * al[r] + ptx::ex2(x[r] - joined(mn));
+            w[r] = ptx::ex2((x[r] + (8.f - yb)) + ev);
+            Fn[r] = ptx::ex2(yb - joined(mn) - 8.f);
           }
           uint32_t pw[S::CP / 4];
 #pragma unroll
@@ -740,7 +738,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
             ok = false;
             break;
           }
-          F = __uint_as_float(evm > 8 ? (uint32_t)(evm - 8) << 23 : 1u << (evm + 14));   // 2^(evm - 127 - 8)
+#pragma unroll
+          for (int r = 0; r < R; ++r) F[r] = Fn[r];
         }
         float one[R];
 #pragma unroll
@@ -872,7 +871,7 @@ cudaError_t launch_t(const AttendArgs &a, int q_limit, int grid, uint8_t *ws, cu
   const uint64_t dims[3] = {(uint64_t)D, (uint64_t)a.hkv, (uint64_t)a.num_pages * a.p};
   const uint64_t strides[2] = {(uint64_t)D, (uint64_t)a.hkv * D};
   const uint32_t box[3] = {(uint32_t)S::W, 1, (uint32_t)(a.p < BN ? a.p : BN)};
-  if (!make_tmap_u8_3d(&tk, a.c.k, dims, strides, box) || !make_tmap_u8_3d(&tv, a.c.v, dims, strides, box))
+  if (!make_tmap_u8_3d(&tk, a.c.k, dims, strides, box, true) || !make_tmap_u8_3d(&tv, a.c.v, dims, strides, box, true))
     return cudaErrorInvalidValue;
   Args g{};
   g.a = a;

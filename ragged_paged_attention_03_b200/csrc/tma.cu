@@ -44,7 +44,7 @@ bool make_tmap_bf16_3d(CUtensorMap *map, const void *base, const uint64_t dims[3
 }
 
 bool make_tmap_u8_3d(CUtensorMap *map, const void *base, const uint64_t dims[3], const uint64_t strides_bytes[2],
-                     const uint32_t box[3]) {
+                     const uint32_t box[3], bool swizzle) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
   cuuint64_t gdim[3] = {dims[0], dims[1], dims[2]};
@@ -53,7 +53,7 @@ bool make_tmap_u8_3d(CUtensorMap *map, const void *base, const uint64_t dims[3],
   cuuint32_t es[3] = {1, 1, 1};
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), gdim, gstride, bx, es,
                   CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  box[0] == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE : box[0] == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                   // no wider than one row: the next bytes are another row's
                   dims[0] >= 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
                                  : dims[0] >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_NONE,

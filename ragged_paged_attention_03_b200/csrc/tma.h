@@ -16,9 +16,9 @@ namespace rpa {
 bool make_tmap_bf16_3d(CUtensorMap *map, const void *base, const uint64_t dims[3],
                        const uint64_t strides_bytes[2], const uint32_t box[3], bool swizzle128);
 
-// An 8-bit tensor map of rank 3, swizzled over the box's inner extent (64 or
+// An 8-bit tensor map of rank 3; swizzle: over the box's inner extent (64 or
 // 128 bytes).
 bool make_tmap_u8_3d(CUtensorMap *map, const void *base, const uint64_t dims[3], const uint64_t strides_bytes[2],
-                     const uint32_t box[3]);
+                     const uint32_t box[3], bool swizzle);
 
 }  // namespace rpa

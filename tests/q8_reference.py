@@ -80,9 +80,6 @@ class Q8Problem:
         e = scale_of(self.v_scales[torch.where(bad, 0, page), h, pos % self.p])
         return torch.where(bad | torch.isnan(e), 1.0, e)
 
-    def v_top(self, s, n, h):
-        return self.v_scale(s, n, h).amax()
-
 
 def make(q_lens, kv_lens, *, hq, hkv, d, p, dtype=torch.bfloat16, causal=True, seed=0, spare=3, extra_width=1,
          poison=True, scale=None, gain=1.0):
@@ -128,10 +125,10 @@ def attend(pr: Q8Problem):
       the same: |out - ref| <= u |out| + A * (2 ds + w), w = 2 * 2^-8 for bf16
       and 2 * 2^-17 for fp32 (weights held to 17 bits or better there),
       plus 2^-16 A (2^-18 for fp32: a row's fp32 sums and exponentials);
-      and, whatever the weights, 2^-30 * 2^ev * sum_j |code_jd| / l over the visible keys, 2^ev the
-      largest V scale and l the softmax sum (its largest weight 1): a weight w, scaled so that
-      w 2^(ev_j - ev) 256 <= 256, is held as four e4m3 parts, each scaled by 16 against the one
-      before, so the last one's smallest step 2^-9 leaves 2^-10 / 16^3 / 256 = 2^-30;
+      and 2^-29 * C * sum_j |code_jd| over the visible keys, C = max_j softmax_j 2^ev_j the row's
+      largest weight times V scale: weights are held relative to C 2^-8 .. C (four e4m3 parts, each
+      16 times finer than the one before: the last one's smallest step 2^-9 leaves 2^-10 / 16^3 / 256
+      = 2^-30 of the largest) or, in fp16, to at least 2^4 for C, with a smallest half step of 2^-25;
       |lse - ref| <= ds + 2^-20 (1 + |lse|).
     """
     t = sum(pr.q_lens)
@@ -166,10 +163,9 @@ def attend(pr: Q8Problem):
                                  q[:, h].abs().amax(-1) * 2.0 ** -21 * kh.abs().sum(-1).amax())
                 out[at:at + a, h] = torch.where(nan[:, None], math.nan, o)
                 lse[at:at + a, h] = torch.where(nan, math.nan, l)
-                vmax = pr.v_top(s, b, h // g)
-                floor = 2.0 ** -30 * (seen.double() @ (vh.abs() / pr.v_scale(s, b, h // g)[:, None])) * vmax
-                tol_o[at:at + a, h] = (half * o.abs() + (pw @ vh.abs()) * (2 * ds[:, None] + w) +
-                                       floor / torch.where(some, total, 1.0)[:, None])
+                vs = pr.v_scale(s, b, h // g)
+                floor = 2.0 ** -29 * (pw * vs).amax(-1)[:, None] * (seen.double() @ (vh.abs() / vs[:, None]))
+                tol_o[at:at + a, h] = half * o.abs() + (pw @ vh.abs()) * (2 * ds[:, None] + w) + floor
                 tol_l[at:at + a, h] = torch.where(some, ds + 2.0 ** -20 * (1 + l.abs()), 0.0)
         at += a
     return out, lse, tol_o, tol_l

@@ -303,6 +303,33 @@ def test_attend_one_loud_token(name):
     Dev(pr).attend().checked(what=name)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("name", ["decode", "decode_d256", "few", "chunk", "chunk_d64", "fresh", "cross_gqa"])
+def test_attend_scales_far_apart(name, dtype):
+    """Rows of one sequence that differ in size by up to 2^60, rows of zeros
+    (scale 2^0) among far smaller ones, and a huge last token, which a causal
+    mask hides from all rows but the last."""
+    pr = problem(name, dtype, gain=1e-6)
+    gen = torch.Generator().manual_seed(5)
+    for s, b in enumerate(pr.kv_lens):
+        if b == 0:
+            continue
+        pos = torch.arange(b)
+        page, slot = pr.table[s].long()[pos // pr.p], pos % pr.p
+        dk = torch.randint(-40, 20, (b, pr.hkv), generator=gen)
+        dv = torch.randint(-30, 31, (b, pr.hkv), generator=gen)
+        if b > 40:
+            dv[-1] += 40
+            dv[b // 2:b // 2 + 8] = -60
+        for scales, d in ((pr.k_scales, dk), (pr.v_scales, dv)):
+            scales[page, :, slot] = (scales[page, :, slot].int() + d).to(torch.uint8)
+        zero = torch.randperm(b, generator=gen)[:b // 8]
+        for codes, scales in ((pr.k_codes, pr.k_scales), (pr.v_codes, pr.v_scales)):
+            codes[page[zero], slot[zero]] = 0
+            scales[page[zero], :, slot[zero]] = 127
+    Dev(pr).attend().checked(what=name)
+
+
 @pytest.mark.parametrize("name", ["decode", "chunk", "chunk_d64", "chunk_d256", "few"])
 def test_attend_bad_pages_read_as_zeros(name):
     pr = problem(name)
