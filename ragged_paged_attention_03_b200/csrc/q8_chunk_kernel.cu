@@ -37,8 +37,10 @@
 //                   fp16 in place
 //   warps 8-11      keys and values: code tiles, landed by TMA, into swizzled fp16 tiles
 //   warp 12         TMEM owner and MMA issue
-//   warp 13         walks the run: segment descriptors for the others, TMA of Q
-//   warp 14         TMA of the code tiles
+//   warp 13, 14     TMA of Q, of the code tiles
+//   warp 15         walks the run and writes its segments down for the others (it waits
+//                   for nothing but their slots: the converters look two blocks ahead,
+//                   into segments whose Q cannot be loaded yet)
 // TMEM (512 columns): S/P of tile 0 | S/P of tile 1 | O of tile 0 | O of tile 1.
 #include <cuda.h>
 #include <math.h>
@@ -88,7 +90,7 @@ struct Bars {
   uint64_t drain;
 };
 
-// One item's part of the CTA's run, written by warp 13 for the others.
+// One item's part of the CTA's run, written by warp 15 for the others.
 struct Seg {
   int32_t seq, hk, item, b0;
   int32_t blocks;                // blocks to run; < 0: the end of the run
@@ -98,7 +100,7 @@ struct Seg {
   int32_t whole;                 // the item begins and ends here
   int32_t pad[2];
 };
-constexpr int kSegUsers = 1 + 1 + 4 + 8;   // warps that release a slot: MMA, TMA, converters, softmax
+constexpr int kSegUsers = 1 + 2 + 4 + 8;   // warps that release a slot: MMA, TMA, converters, softmax
 
 struct PartHead {
   int32_t seq, hk, item, begin;
@@ -403,9 +405,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
-    if (warp == 13) {
-      // ---------------------------------------------------------- TMA of Q
-      const uint64_t once = ptx::l2_evict_first_policy();
+    if (warp == 15) {
+      // ------------------------------------------------------- the run
       Run run;
       run.g = &g;
       run.n = n;
@@ -415,14 +416,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       run.blk = (int)s_scan[19];
       run.left = count;
       run.load();
-      int uses[2] = {0, 0};
-      const uint32_t bytes = (uint32_t)(S::kHalves * 128 * g.tpt * G);
-      bool ok = true, more = true;
-      for (; ok && more; ++segs) {
+      for (bool more = true; more; ++segs) {
         const int slot = segs % kSegSlots;
-        if (segs >= kSegSlots)
-          ok = wait_warp(&bars->seg_empty[slot], (uint32_t)(((segs / kSegSlots) & 1) ^ 1), abort_flag, err);
-        if (!ok) break;
+        if (segs >= kSegSlots &&
+            !wait_warp(&bars->seg_empty[slot], (uint32_t)(((segs / kSegSlots) & 1) ^ 1), abort_flag, err))
+          break;
         more = run.next();
         if (lane == 0) {
           Seg d{};
@@ -435,23 +433,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::mbar_arrive(&bars->seg_full[slot]);
         }
         __syncwarp();
-        if (!more) break;
+      }
+    } else if (warp == 13) {
+      // ---------------------------------------------------------- TMA of Q
+      const uint64_t once = ptx::l2_evict_first_policy();
+      int uses0 = 0, uses1 = 0;
+      const uint32_t bytes = (uint32_t)(S::kHalves * 128 * g.tpt * G);
+      bool ok = true;
+      while (ok) {
+        const Seg *sg = next_seg();
+        if (sg == nullptr) break;
+        const int n0 = sg->nt[0], n1 = sg->nt[1], h0 = sg->hk * G, tok = sg->q0 + sg->row0;
+        done_seg();
         for (int t = 0; t < 2; ++t) {
-          const int nt = t ? run.nt[1] : run.nt[0];
-          if (!ok || nt == 0) continue;
-          const int u = t ? uses[1] : uses[0];
+          if (!ok || (t ? n1 : n0) == 0) continue;
+          const int u = t ? uses1 : uses0;
           if (u > 0) ok = wait_warp(&bars->q_empty[t], (uint32_t)((u - 1) & 1), abort_flag, err);
           if (!ok) continue;
           ptx::mbar_arrive_expect_tx_elect(&bars->q_full[t], bytes);
           for (int h = 0; h < S::kHalves; ++h)
-            ptx::tma_load_3d_hint_elect(sQ + t * S::kQBytes + h * BM * 128, &tm_q, &bars->q_full[t], h * 64,
-                                        run.hk * G, run.q0 + run.row0 + t * g.tpt, once);
-          if (t) ++uses[1]; else ++uses[0];
+            ptx::tma_load_3d_hint_elect(sQ + t * S::kQBytes + h * BM * 128, &tm_q, &bars->q_full[t], h * 64, h0,
+                                        tok + t * g.tpt, once);
+          if (t) ++uses1; else ++uses0;
         }
       }
       // queued copies land before the CTA ends
-      for (int t = 0; t < 2; ++t)
-        if (uses[t] > 0) ptx::mbar_wait(&bars->q_full[t], (uint32_t)((uses[t] - 1) & 1));
+      if (uses0 > 0) ptx::mbar_wait(&bars->q_full[0], (uint32_t)((uses0 - 1) & 1));
+      if (uses1 > 0) ptx::mbar_wait(&bars->q_full[1], (uint32_t)((uses1 - 1) & 1));
       __syncwarp();
     } else if (warp == 14) {
       // ------------------------------------------------- TMA of the codes

@@ -222,6 +222,8 @@ G = dict(  # name: q_lens, kv_lens, hq, hkv, d, p, causal
     cross_gqa=([100, 257], [1000, 129], 8, 2, 128, 16, False),
     cross_d256=([100, 57], [300, 129], 4, 2, 256, 16, False),
     fresh=([513, 256], [513, 256], 4, 1, 128, 16, True),
+    many_short=([17 + i % 30 for i in range(100)], [17 + i % 30 + (i % 7) * 20 for i in range(100)], 16, 16, 64, 16, True),
+    many_short_gqa=([9 + i % 70 for i in range(60)], [9 + i % 70 for i in range(60)], 32, 8, 128, 16, True),
     long_ctx=([20], [6000], 4, 1, 128, 16, True),
 )
 
