@@ -236,11 +236,11 @@ __device__ __forceinline__ void issue_qk(uint32_t tS, uint64_t dq, uint64_t dk) 
   }
 }
 
-// f16x2 with 2^(e - top) in both halves (0 below fp16's range), NaN if `nan`.
+// 2^(e - top) as fp16 bits (0 below fp16's range; a byte of no key may lie above
+// top: 1), NaN if `nan`.
 __device__ __forceinline__ uint32_t half_factor(int e, int top, bool nan) {
-  const int d = e - top;
-  const uint32_t h = nan ? 0x7fffu : d >= -14 ? (uint32_t)(15 + d) << 10 : d >= -24 ? 1u << (24 + d) : 0u;
-  return h | (h << 16);
+  const int d = min(e - top, 0);
+  return nan ? 0x7fffu : d >= -14 ? (uint32_t)(15 + d) << 10 : d >= -24 ? 1u << (24 + d) : 0u;
 }
 __device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -629,43 +629,49 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++cursor.b;
       return c;
     };
+    // the page of the lane's keys as the table has it (checked when it is used, so
+    // that nothing waits for the load), -1: no key
     auto page_of = [&](const Block &c) -> int {
       const int pos = c.b * BN + lane * 4;
-      if (c.b < 0 || pos >= c.kv) return -1;
-      const int pg = c.pt[pos >> a.p_shift];
-      if (pg >= 0 && pg < a.num_pages) return pg;
-      raise(err, RPA_DEV_BAD_PAGE);
-      return -1;
+      return c.b < 0 || pos >= c.kv ? -1 : c.pt[pos >> a.p_shift];
     };
+    auto readable = [&](int pg) -> bool { return (unsigned)pg < (unsigned)a.num_pages; };
     auto scales_of = [&](const Block &c, int pg, const uint8_t *src) -> uint32_t {
-      if (pg < 0) return 0;
+      if (!readable(pg)) return 0;
       const int pos = c.b * BN + lane * 4;
       return *reinterpret_cast<const uint32_t *>(src + ((size_t)pg * a.hkv + c.hk) * a.p + (pos & (a.p - 1)));
     };
-    // code tile -> fp16 tile; rows from `keys` on, which no copy filled, become zeros
+    // what each lane's part of a row goes through: rows differ by their key's factor
+    const uint32_t dup = lrow & 1 ? 0x3232u : 0x1010u;
+    const int c0 = 2 * (lcol & 3), swp = (lcol >> 2) & 1;
+    // code tile -> fp16 tile, key by key times 2^(scale - top); rows from `keys` on, which
+    // no copy filled, become zeros
     auto convert = [&](uint8_t *dst, const uint8_t *src, uint32_t scales, uint32_t nans, int top, int keys,
                        bool wide) {
+      // the factors of keys 4 lane .. + 3
+      uint32_t f01, f23;
+      {
+        uint32_t h[4];
 #pragma unroll
+        for (int k = 0; k < 4; ++k)
+          h[k] = half_factor(wide ? top : (int)((scales >> (8 * k)) & 255u), top, ((nans >> (8 * k)) & 255u) != 0);
+        f01 = h[0] | (h[1] << 16);
+        f23 = h[2] | (h[3] << 16);
+      }
+#pragma unroll 2
       for (int i = 0; i < NU; ++i) {
         const int row = (i * 4 + cw) * RU + lrow;
         uint4 x = *reinterpret_cast<const uint4 *>(src + row * D + lcol * 16);
+        const uint32_t a01 = __shfl_sync(0xffffffffu, f01, row >> 2), a23 = __shfl_sync(0xffffffffu, f23, row >> 2);
+        const uint32_t f = __byte_perm(row & 2 ? a23 : a01, 0u, dup);
         if (row >= keys) x = make_uint4(0, 0, 0, 0);
-        const int sh = (row & 3) * 8;
-        const int e = (int)((__shfl_sync(0xffffffffu, scales, row >> 2) >> sh) & 255u);
-        const bool nan = ((__shfl_sync(0xffffffffu, nans, row >> 2) >> sh) & 255u) != 0;
-        const uint32_t f = row < keys ? half_factor(wide ? top : e, top, nan) : 0u;
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        uint32_t h[8];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          h[2 * q] = mul_h2(codes_h2(w[q] & 0xffffu), f);
-          h[2 * q + 1] = mul_h2(codes_h2(w[q] >> 16), f);
-        }
-        // values 16 lcol .. + 15: chunks 2 (lcol % 4), + 1 of column tile lcol / 4; lanes
-        // of odd column tiles store theirs in the other order (no bank is hit twice)
-        const int c0 = 2 * (lcol & 3), swp = (lcol >> 2) & 1;
+        const uint4 u0 = make_uint4(mul_h2(codes_h2(x.x), f), mul_h2(codes_h2(x.x >> 16), f),
+                                    mul_h2(codes_h2(x.y), f), mul_h2(codes_h2(x.y >> 16), f));
+        const uint4 u1 = make_uint4(mul_h2(codes_h2(x.z), f), mul_h2(codes_h2(x.z >> 16), f),
+                                    mul_h2(codes_h2(x.w), f), mul_h2(codes_h2(x.w >> 16), f));
+        // values 16 lcol .. + 15: chunks c0, c0 + 1 of column tile lcol / 4; lanes of odd
+        // column tiles store theirs in the other order (no bank is hit twice)
         uint8_t *p = dst + (lcol >> 2) * BN * 128 + row * 128;
-        const uint4 u0 = make_uint4(h[0], h[1], h[2], h[3]), u1 = make_uint4(h[4], h[5], h[6], h[7]);
         *reinterpret_cast<uint4 *>(p + (((c0 + swp) ^ (row & 7)) << 4)) = swp ? u1 : u0;
         *reinterpret_cast<uint4 *>(p + (((c0 + 1 - swp) ^ (row & 7)) << 4)) = swp ? u0 : u1;
       }
@@ -682,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int ek = 0, ev = 0, ek0 = 255, ev0 = 255;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const bool key = pg >= 0 && cur.b * BN + lane * 4 + j < cur.kv;
+        const bool key = readable(pg) && cur.b * BN + lane * 4 + j < cur.kv;
         const uint32_t k8 = (ks >> (8 * j)) & 255u, v8 = (vs >> (8 * j)) & 255u;
         if (key && (k8 == kScaleNan || v8 == kScaleNan)) nans |= 255u << (8 * j);
         if (key && k8 != kScaleNan) {
@@ -808,122 +814,148 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int ek = s_exp[eslot * 2] & 255, ev = s_exp[eslot * 2 + 1] & 255;
         const bool wide_k = s_exp[eslot * 2] >= kWideBit, wide_v = s_exp[eslot * 2 + 1] >= kWideBit;
-        // scale byte of key i of a wide tile; -1: not seen, or its page is outside the pool
+        // For a wide tile (whose codes carry no scale): the scale byte of key i, -1 if it
+        // is not seen or its page is outside the pool
         auto scale_byte = [&](const uint8_t *src, int i) -> int {
           const int pos = (b0 + j) * BN + i;
           const int pg = pos < end ? pt[pos >> a.p_shift] : -1;
           if (pg < 0 || pg >= a.num_pages) return -1;
           return src[((size_t)pg * a.hkv + hk) * a.p + (pos & (a.p - 1))];
         };
+        auto wide_score = [&](const uint32_t (&v)[8], int vi, int i, int lim, float sc, int top) -> float {
+          if (i >= lim) return -INFINITY;
+          const int d = wide_k ? min(scale_byte(a.c.ks, i) - top, 0) : 0;   // > 0: a NaN key, NaN already
+          return __uint_as_float(v[vi]) * (d < -126 ? 0.f : __uint_as_float((uint32_t)(127 + d) << 23)) * sc;
+        };
+        // V scale of key i relative to `ref`; the tile's own `top` where its values carry theirs
+        auto wide_ev = [&](int i, int top, int ref) -> float {
+          return (float)((wide_v ? scale_byte(a.c.vs, i) : top) - ref);
+        };
         ptx::tc_fence_after();
-        float x[BN];
-#pragma unroll
-        for (int cc = 0; cc < BN / 32; ++cc)
-          ptx::tmem_ld32(tS + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[cc * 32]));
-        ptx::tmem_ld_wait();
-        if (wide_k) {
-#pragma unroll
-          for (int i = 0; i < BN; ++i) {
-            const int d = scale_byte(a.c.ks, i) - ek;      // > 0: a NaN key, whose score is NaN already
-            x[i] *= d < -126 ? 0.f : __uint_as_float((uint32_t)(127 + min(d, 0)) << 23);
-          }
-        }
         const int lim = min(BN, end - (b0 + j) * BN);
-        if (__any_sync(0xffffffffu, lim < BN)) {
-#pragma unroll
-          for (int i = 0; i < BN; ++i) x[i] = i < lim ? x[i] : -INFINITY;
-        }
-        float mq[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-        for (int i = 4; i < BN; i += 8) {
-          mq[0] = ptx::fmax3(mq[0], x[i], x[i + 1]);
-          mq[1] = ptx::fmax3(mq[1], x[i + 2], x[i + 3]);
-          if (i + 4 < BN) {
-            mq[2] = ptx::fmax3(mq[2], x[i + 4], x[i + 5]);
-            mq[3] = ptx::fmax3(mq[3], x[i + 6], x[i + 7]);
-          }
-        }
         // never 0, which would make NaN of a masked score
         float sc = qf * scale_value((uint32_t)ek);
         if (sc < 1e-37f) sc = 1e-37f;
-        const float mx = ptx::fmax3(mq[0], mq[1], fmaxf(mq[2], mq[3])) * sc;
-        // the block's largest contribution, relative to 2^ev
-        float my = mx;
-        if (wide_v) {
-          my = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < BN; ++i) my = fmaxf(my, fmaf(x[i], sc, (float)(scale_byte(a.c.vs, i) - ev)));
-        }
-        const float m_new = fmaxf(m, mx);
-        // contributions of the row may pass the units of O by 2^kRescale
-        const bool need = m_new > m + kRescale || my + (float)(ev - evr) > m + kRescale;
-        if (__any_sync(0xffffffffu, need)) {
-          // PV(t, j - 1) is complete: s_full(t, j) was committed after QK(t, j), issued behind it.
-          // The new units: the larger of the old ones and the block's largest contribution
-          // (a row that has seen nothing has no old ones)
-          const float top = m == -INFINITY ? my + (float)ev : fmaxf(m + (float)evr, my + (float)ev);
-          const int evn = m_new == -INFINITY || top == -INFINITY ? evr : (int)ceilf(fmaxf(top - m_new, -300.f));
-          const float am = m == -INFINITY ? 0.f : ptx::ex2(m - m_new);
-          const float alpha = m == -INFINITY ? 0.f : ptx::ex2((m - m_new) + (float)(evr - evn));
-          if (j > 0) {
+        // Moves m (and the units of O, evr) to what the block needs: mx its largest score, my
+        // its largest score with the V scale, relative to 2^ev.
+        auto take_max = [&](float mx, float my) {
+          const float m_new = fmaxf(m, mx);
+          // contributions of the row may pass the units of O by 2^kRescale
+          const bool need = m_new > m + kRescale || my + (float)(ev - evr) > m + kRescale;
+          if (__any_sync(0xffffffffu, need)) {
+            // PV(t, j - 1) is complete: s_full(t, j) was committed after QK(t, j), issued behind it.
+            // The new units: the larger of the old ones and the block's largest contribution
+            // (a row that has seen nothing has no old ones)
+            const float top = m == -INFINITY ? my + (float)ev : fmaxf(m + (float)evr, my + (float)ev);
+            const int evn = m_new == -INFINITY || top == -INFINITY ? evr : (int)ceilf(fmaxf(top - m_new, -300.f));
+            const float am = m == -INFINITY ? 0.f : ptx::ex2(m - m_new);
+            const float alpha = m == -INFINITY ? 0.f : ptx::ex2((m - m_new) + (float)(evr - evn));
+            if (j > 0) {
 #pragma unroll 1
-            for (int cc = 0; cc < D / 32; ++cc) {
-              uint32_t r[32];
-              ptx::tmem_ld32(tO + cc * 32, r);
-              ptx::tmem_ld_wait();
+              for (int cc = 0; cc < D / 32; ++cc) {
+                uint32_t r[32];
+                ptx::tmem_ld32(tO + cc * 32, r);
+                ptx::tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
-              ptx::tmem_st32(tO + cc * 32, r);
+                for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+                ptx::tmem_st32(tO + cc * 32, r);
+              }
             }
+            l *= am;
+            m = m_new;
+            evr = evn;
           }
-          l *= am;
-          m = m_new;
-          evr = evn;
-        }
+        };
         // values more than 2^64 below the row's units count as that small (the sum
         // needs the weights above fp32's underflow)
-        const int dv = max(ev - evr, -64);
-        float shift = (m == -INFINITY ? 0.f : -m) + (float)(kBase + dv);
-        float wide_sum = 0.f;
-        if (wide_v) {
-          // the sum of the bare weights here, and x the exponents with the V scales
-          shift -= (float)dv;
+        auto lift = [&]() -> int { return max(ev - evr, -64); };
+        if (!(wide_k || wide_v)) {                    // the same for the whole tile
+          float x[BN];
 #pragma unroll
-          for (int i = 0; i < BN; ++i) {
-            const float y = fmaf(x[i], sc, shift);
-            wide_sum += ptx::ex2(y);
-            x[i] = y + (float)(scale_byte(a.c.vs, i) - evr);
+          for (int cc = 0; cc < BN / 32; ++cc)
+            ptx::tmem_ld32(tS + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[cc * 32]));
+          ptx::tmem_ld_wait();
+          if (__any_sync(0xffffffffu, lim < BN)) {
+#pragma unroll
+            for (int i = 0; i < BN; ++i) x[i] = i < lim ? x[i] : -INFINITY;
           }
-          sc = 1.f;
-          shift = 0.f;
+          float mq[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+          for (int i = 4; i < BN; i += 8) {
+            mq[0] = ptx::fmax3(mq[0], x[i], x[i + 1]);
+            mq[1] = ptx::fmax3(mq[1], x[i + 2], x[i + 3]);
+            if (i + 4 < BN) {
+              mq[2] = ptx::fmax3(mq[2], x[i + 4], x[i + 5]);
+              mq[3] = ptx::fmax3(mq[3], x[i + 6], x[i + 7]);
+            }
+          }
+          const float mx = ptx::fmax3(mq[0], mq[1], fmaxf(mq[2], mq[3])) * sc;
+          take_max(mx, mx);
+          const int dv = lift();
+          const float shift = (m == -INFINITY ? 0.f : -m) + (float)(kBase + dv);
+          const uint64_t scale2 = ptx::f2_pack(sc, sc);
+          const uint64_t shift2 = ptx::f2_pack(shift, shift);
+          uint64_t sp2[4] = {0, 0, 0, 0};
+          uint32_t pk[BN / 2];
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+            for (int i = hf * (BN / 2); i < (hf + 1) * (BN / 2); i += 2) {
+              float a0, a1;
+              ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(x[i], x[i + 1]), scale2, shift2), a0, a1);
+              const float p0 = ptx::ex2(a0), p1 = ptx::ex2(a1);
+              sp2[(i >> 1) & 3] = ptx::f2_add(sp2[(i >> 1) & 3], ptx::f2_pack(p0, p1));
+              pk[i >> 1] = ptx::pack_f16(p0, p1);
+            }
+            ptx::tmem_st32(tS + hf * 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[hf * 32]));
+            if (hf == 0) {
+              ptx::tmem_st_wait();
+              ptx::tc_fence_before();
+              ptx::mbar_arrive(&bars->p_half[t]);
+            }
+          }
+          float sp[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) ptx::f2_unpack(sp2[k], sp[2 * k], sp[2 * k + 1]);
+          const float sum = ((sp[0] + sp[1]) + (sp[2] + sp[3])) + ((sp[4] + sp[5]) + (sp[6] + sp[7]));
+          l += sum * ptx::ex2((float)-dv);            // weights of this block carry 2^dv
+        } else {
+          float mx = -INFINITY, my = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < BN; c += 8) {
+            uint32_t v[8];
+            ptx::tmem_ld8(tS + c, v, 0);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float y = wide_score(v, i, c + i, lim, sc, ek);
+              mx = fmaxf(mx, y);
+              my = fmaxf(my, y + wide_ev(c + i, ev, ev));
+            }
+          }
+          take_max(mx, my);
+          // the sum of the bare weights; P with each key's scale
+          const float shift = (m == -INFINITY ? 0.f : -m) + (float)kBase;
+          float sum = 0.f;
+#pragma unroll 1
+          for (int c = 0; c < BN; c += 8) {
+            uint32_t v[8], pk[4];
+            ptx::tmem_ld8(tS + c, v, 0);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+              const float y0 = wide_score(v, i, c + i, lim, sc, ek) + shift;
+              const float y1 = wide_score(v, i + 1, c + i + 1, lim, sc, ek) + shift;
+              sum += ptx::ex2(y0) + ptx::ex2(y1);
+              pk[i / 2] = ptx::pack_f16(ptx::ex2(y0 + wide_ev(c + i, ev, evr)), ptx::ex2(y1 + wide_ev(c + i + 1, ev, evr)));
+            }
+            ptx::tmem_st4(tS + c / 2, pk);            // behind what has been read
+          }
+          ptx::tmem_st_wait();
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(&bars->p_half[t]);
+          l += sum;
         }
-        const uint64_t scale2 = ptx::f2_pack(sc, sc);
-        const uint64_t shift2 = ptx::f2_pack(shift, shift);
-        uint64_t sp2[4] = {0, 0, 0, 0};
-        uint32_t pk[BN / 2];
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-#pragma unroll
-          for (int i = hf * (BN / 2); i < (hf + 1) * (BN / 2); i += 2) {
-            float a0, a1;
-            ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(x[i], x[i + 1]), scale2, shift2), a0, a1);
-            float p0 = ptx::ex2(a0), p1 = ptx::ex2(a1);
-            sp2[(i >> 1) & 3] = ptx::f2_add(sp2[(i >> 1) & 3], ptx::f2_pack(p0, p1));
-            pk[i >> 1] = ptx::pack_f16(p0, p1);
-          }
-          ptx::tmem_st32(tS + hf * 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[hf * 32]));
-          if (hf == 0) {
-            ptx::tmem_st_wait();
-            ptx::tc_fence_before();
-            ptx::mbar_arrive(&bars->p_half[t]);
-          }
-        }
-        float sp[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) ptx::f2_unpack(sp2[k], sp[2 * k], sp[2 * k + 1]);
-        const float sum = ((sp[0] + sp[1]) + (sp[2] + sp[3])) + ((sp[4] + sp[5]) + (sp[6] + sp[7]));
-        // weights of this block carry 2^dv
-        l += wide_v ? wide_sum : sum * ptx::ex2((float)-dv);
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
         ptx::mbar_arrive(&bars->p_full[t]);
