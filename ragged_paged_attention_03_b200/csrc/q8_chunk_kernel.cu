@@ -115,12 +115,14 @@ struct Args {
   float4 *o;             // [2 * ctas][D / 4][256]
 };
 
+// Waits for a phase, for at most kWaitTries polls (a second or more): false, with
+// RPA_DEV_TIMEOUT raised, when they run out or another warp gave up.  Kept short:
+// the kernel's roles share one instruction cache.
+constexpr uint32_t kWaitTries = 1u << 25;
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort_flag, uint32_t *err) {
-  if (ptx::mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = ptx::globaltimer();
+  uint32_t n = 0;
   while (!ptx::mbar_try_wait(bar, parity)) {
-    if (*abort_flag) return false;
-    if (ptx::globaltimer() - t0 > ptx::kWaitLimitNs) {
+    if ((++n & 63) == 0 && (*abort_flag || n >= kWaitTries)) {
       *abort_flag = 1;
       raise(err, RPA_DEV_TIMEOUT);
       return false;
@@ -143,7 +145,9 @@ __device__ __forceinline__ int64_t floor_sum128(int64_t n, int64_t a, int64_t b)
   // i = 128 j + k: floor((ar i + br) / 128) = ar j + floor((ar k + br) / 128)
   int64_t whole = 0, part = 0;
   if (turns > 0)
+#pragma unroll 1
     for (int k = 0; k < 128; ++k) whole += (ar * k + br) >> 7;
+#pragma unroll 1
   for (int k = 0; k < rest; ++k) part += (ar * k + br) >> 7;
   return sum + turns * whole + (int64_t)ar * 128 * (turns * (turns - 1) / 2) + part + (int64_t)ar * turns * rest;
 }
@@ -225,16 +229,6 @@ struct Run {
   }
   __device__ __forceinline__ int blocks() const { return max(nt[0], nt[1]); }
 };
-
-template <int D>
-__device__ __forceinline__ void issue_qk(uint32_t tS, uint64_t dq, uint64_t dk) {
-  constexpr uint32_t idesc = ptx::umma_idesc_f16(128, BN, false);
-#pragma unroll
-  for (int ks = 0; ks < D / 16; ++ks) {
-    const uint32_t off = ((ks >> 2) * BM * 128 + (ks & 3) * 32) >> 4;
-    ptx::umma_ss_elect(tS, dq + off, dk + off, idesc, ks > 0 ? 1u : 0u);
-  }
-}
 
 // 2^(e - top) as fp16 bits (0 below fp16's range; a byte of no key may lie above
 // top: 1), NaN if `nan`.
@@ -520,82 +514,68 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dq0 = ptx::umma_desc_sw128(ptx::smem_u32(sQ), 16, 1024);
       const uint64_t dk0 = ptx::umma_desc_sw128(ptx::smem_u32(sK), 16, 1024);
       const uint64_t dv0 = ptx::umma_desc_sw128(ptx::smem_u32(sV), BN * 128, 1024);
-      int gb = 0, gt0 = 0, gt1 = 0, ep0 = 0, ep1 = 0;
+      int gb = 0, gt[2] = {0, 0}, ep[2] = {0, 0};
       bool ok = true;
-      auto qk = [&](int t, int blk, bool wait) -> bool {
-        const int st = blk % NSK;
-        if (wait && !wait_warp(&bars->k_full[st], (uint32_t)((blk / NSK) & 1), abort_flag, err)) return false;
-        ptx::tc_fence_after();
-        issue_qk<D>(tmem + t * 128, dq0 + (uint64_t)((t * S::kQBytes) >> 4),
-                    dk0 + (uint64_t)((st * S::kKVBytes) >> 4));
-        ptx::umma_commit_elect(&bars->s_full[t]);
-        return true;
-      };
-      auto pv = [&](int t, int blk, int tblk, bool first, bool wait) -> bool {
-        constexpr uint32_t idesc = ptx::umma_idesc_f16(128, D, true);
-        const int st = blk % NSV;
-        const uint32_t tS = tmem + t * 128, tO = tmem + S::kColO + t * D;
-        if (!wait_warp(&bars->p_half[t], (uint32_t)(tblk & 1), abort_flag, err)) return false;
-        if (wait && !wait_warp(&bars->v_full[st], (uint32_t)((blk / NSV) & 1), abort_flag, err)) return false;
-        ptx::tc_fence_after();
-        const uint64_t dv = dv0 + (uint64_t)((st * S::kKVBytes) >> 4);
-#pragma unroll
-        for (int kk = 0; kk < BN / 32; ++kk)
-          ptx::umma_ts_elect(tO, tS + kk * 8, dv + (uint64_t)((kk * 16 * 128) >> 4), idesc, (!first || kk > 0) ? 1u : 0u);
-        if (!wait_warp(&bars->p_full[t], (uint32_t)(tblk & 1), abort_flag, err)) return false;
-        ptx::tc_fence_after();
-#pragma unroll
-        for (int kk = BN / 32; kk < BN / 16; ++kk)
-          ptx::umma_ts_elect(tO, tS + kk * 8, dv + (uint64_t)((kk * 16 * 128) >> 4), idesc, 1u);
-        return true;
-      };
       while (ok) {
         const Seg *sg = next_seg();
         if (sg == nullptr) break;
         const int n0 = sg->nt[0], n1 = sg->nt[1], nb = sg->blocks;
         done_seg();
-        if (nb == 0) continue;
-        if (n0 > 0) {
-          ok = wait_warp(&bars->qc_full[0], (uint32_t)(ep0 & 1), abort_flag, err) && qk(0, gb, true);
-          if (ok && n0 == 1) ptx::umma_commit_elect(&bars->q_empty[0]);
-        }
-        if (ok && n1 > 0) {
-          ok = wait_warp(&bars->qc_full[1], (uint32_t)(ep1 & 1), abort_flag, err) && qk(1, gb, n0 == 0);
-          if (ok && n1 == 1) ptx::umma_commit_elect(&bars->q_empty[1]);
-        }
-        if (ok) ptx::umma_commit_elect(&bars->k_empty[gb % NSK]);
-        if (ok && n0 > 0) {
-          if (ep0 > 0) ok = wait_warp(&bars->o_free[0], (uint32_t)((ep0 - 1) & 1), abort_flag, err);
-          ok = ok && pv(0, gb, gt0, true, true);
-          if (ok && n0 == 1) ptx::umma_commit_elect(&bars->pv_done[0]);
-        }
-        for (int j = 0; ok && j < nb; ++j) {
-          const bool k_waited = j + 1 < n0;
-          if (j + 1 < n0) {
-            ok = qk(0, gb + j + 1, true);
-            if (ok && j + 2 == n0) ptx::umma_commit_elect(&bars->q_empty[0]);
+        // one QK and one PV a turn: turn (j, 0) is QK0(j+1) PV1(j), turn (j, 1) QK1(j+1) PV0(j+1)
+#pragma unroll 1
+        for (int turn = -2; ok && turn < 2 * nb; ++turn) {
+          const int t = turn & 1, u = t ^ 1, kb = (turn >> 1) + 1, vb = kb - u;   // tiles and blocks
+          const int nk = t ? n1 : n0, nv = t ? n0 : n1;
+          if (kb < nk) {
+            const int st = (gb + kb) % NSK;
+            if (kb == 0) ok = wait_warp(&bars->qc_full[t], (uint32_t)((t ? ep[1] : ep[0]) & 1), abort_flag, err);
+            ok = ok && wait_warp(&bars->k_full[st], (uint32_t)(((gb + kb) / NSK) & 1), abort_flag, err);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            const uint64_t dq = dq0 + (uint64_t)((t * S::kQBytes) >> 4), dk = dk0 + (uint64_t)((st * S::kKVBytes) >> 4);
+            constexpr uint32_t idesc = ptx::umma_idesc_f16(128, BN, false);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint32_t off = ((ks >> 2) * BM * 128 + (ks & 3) * 32) >> 4;
+              ptx::umma_ss_elect(tmem + t * 128, dq + off, dk + off, idesc, ks > 0 ? 1u : 0u);
+            }
+            ptx::umma_commit_elect(&bars->s_full[t]);
+            if (kb + 1 == nk) ptx::umma_commit_elect(&bars->q_empty[t]);
           }
-          if (ok && j < n1) {
-            if (j == 0 && ep1 > 0) ok = wait_warp(&bars->o_free[1], (uint32_t)((ep1 - 1) & 1), abort_flag, err);
-            ok = ok && pv(1, gb + j, gt1 + j, j == 0, j >= n0);
-            if (ok && j + 1 == n1) ptx::umma_commit_elect(&bars->pv_done[1]);
+          if (t == 1 && kb < nb) ptx::umma_commit_elect(&bars->k_empty[(gb + kb) % NSK]);
+          if (vb >= 0 && vb < nv) {
+            const int st = (gb + vb) % NSV;
+            const uint32_t ph = (uint32_t)(((u ? gt[1] : gt[0]) + vb) & 1);
+            const int e = u ? ep[1] : ep[0];
+            // O of the tile is overwritten by the segment's first PV: it must have been read
+            if (vb == 0 && e > 0) ok = wait_warp(&bars->o_free[u], (uint32_t)((e - 1) & 1), abort_flag, err);
+            // P arrives in two halves: keys 0..63 feed the first k-steps
+            ok = ok && wait_warp(&bars->v_full[st], (uint32_t)(((gb + vb) / NSV) & 1), abort_flag, err) &&
+                 wait_warp(&bars->p_half[u], ph, abort_flag, err);
+            if (!ok) break;
+            constexpr uint32_t idesc = ptx::umma_idesc_f16(128, D, true);
+            const uint32_t tS = tmem + u * 128, tO = tmem + S::kColO + u * D;
+            const uint64_t dv = dv0 + (uint64_t)((st * S::kKVBytes) >> 4);
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < BN / 32; ++kk)
+              ptx::umma_ts_elect(tO, tS + kk * 8, dv + (uint64_t)((kk * 16 * 128) >> 4), idesc,
+                                 vb > 0 || kk > 0 ? 1u : 0u);
+            ok = wait_warp(&bars->p_full[u], ph, abort_flag, err);
+            if (!ok) break;
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int kk = BN / 32; kk < BN / 16; ++kk)
+              ptx::umma_ts_elect(tO, tS + kk * 8, dv + (uint64_t)((kk * 16 * 128) >> 4), idesc, 1u);
+            if (vb + 1 == nv) ptx::umma_commit_elect(&bars->pv_done[u]);
           }
-          if (ok) ptx::umma_commit_elect(&bars->v_empty[(gb + j) % NSV]);
-          if (ok && j + 1 < n1) {
-            ok = qk(1, gb + j + 1, !k_waited);
-            if (ok && j + 2 == n1) ptx::umma_commit_elect(&bars->q_empty[1]);
-          }
-          if (ok && j + 1 < nb) ptx::umma_commit_elect(&bars->k_empty[(gb + j + 1) % NSK]);
-          if (ok && j + 1 < n0) {
-            ok = pv(0, gb + j + 1, gt0 + j + 1, false, true);
-            if (ok && j + 2 == n0) ptx::umma_commit_elect(&bars->pv_done[0]);
-          }
+          if (t == 0 && vb >= 0) ptx::umma_commit_elect(&bars->v_empty[(gb + vb) % NSV]);   // both PVs are issued
         }
         gb += nb;
-        gt0 += n0;
-        gt1 += n1;
-        ep0 += n0 > 0 ? 1 : 0;
-        ep1 += n1 > 0 ? 1 : 0;
+        gt[0] += n0;
+        gt[1] += n1;
+        ep[0] += n0 > 0 ? 1 : 0;
+        ep[1] += n1 > 0 ? 1 : 0;
       }
       ptx::umma_commit_elect(&bars->drain);
       ptx::mbar_wait(&bars->drain, 0);
@@ -704,29 +684,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       ev = __reduce_max_sync(0xffffffffu, ev);
       const bool wk = ek - __reduce_min_sync(0xffffffffu, ek0) > kWide;
       const bool wv = ev - __reduce_min_sync(0xffffffffu, ev0) > kWide;
-      const int sk = gb % NSK, sv = gb % NSV;
-      if (gb >= NSK && !wait_warp(&bars->k_empty[sk], (uint32_t)(((gb / NSK) & 1) ^ 1), abort_flag, err)) break;
-      if (warp == 8 && lane == 0) {
-        // free: QK of block gb - 4 or a later one is done for both tiles, and was issued
-        // behind the P of every block up to gb - 5
-        s_exp[(gb % kExpSlots) * 2] = ek | (wk ? kWideBit : 0);
-        s_exp[(gb % kExpSlots) * 2 + 1] = ev | (wv ? kWideBit : 0);
-        ptx::mbar_arrive(&bars->e_full[gb % kExpSlots]);
-      }
       const int keys = cur.kv - cur.b * BN;
-      const int ck = 2 * gb % S::NST, cv = (2 * gb + 1) % S::NST;
-      if (!wait_warp(&bars->c_full[ck], (uint32_t)((2 * gb / S::NST) & 1), abort_flag, err)) break;
-      convert(sK + sk * S::kKVBytes, sC + ck * S::kCodes, ks, nans, ek, keys, wk);
-      ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(&bars->k_full[sk]);
-      ptx::mbar_arrive(&bars->c_empty[ck]);
-      if (gb >= NSV && !wait_warp(&bars->v_empty[sv], (uint32_t)(((gb / NSV) & 1) ^ 1), abort_flag, err)) break;
-      if (!wait_warp(&bars->c_full[cv], (uint32_t)(((2 * gb + 1) / S::NST) & 1), abort_flag, err)) break;
-      // the weight of a NaN key is NaN where it is seen; its codes are zeros, its scale 0 here
-      convert(sV + sv * S::kKVBytes, sC + cv * S::kCodes, vs & ~nans, 0u, ev, keys, wv);
-      ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(&bars->v_full[sv]);
-      ptx::mbar_arrive(&bars->c_empty[cv]);
+      const uint32_t ph = (uint32_t)(((gb / NSK) & 1) ^ 1);
+      bool ok = true;
+#pragma unroll 1
+      for (int v = 0; ok && v < 2; ++v) {
+        const int st = gb % NSK, use = 2 * gb + v, cs = use % S::NST;
+        ok = gb < NSK || wait_warp(v ? &bars->v_empty[st] : &bars->k_empty[st], ph, abort_flag, err);
+        if (ok && v == 0 && warp == 8 && lane == 0) {
+          // free: QK of block gb - 4 or a later one is done for both tiles, and was issued
+          // behind the P of every block up to gb - 5
+          s_exp[(gb % kExpSlots) * 2] = ek | (wk ? kWideBit : 0);
+          s_exp[(gb % kExpSlots) * 2 + 1] = ev | (wv ? kWideBit : 0);
+          ptx::mbar_arrive(&bars->e_full[gb % kExpSlots]);
+        }
+        ok = ok && wait_warp(&bars->c_full[cs], (uint32_t)((use / S::NST) & 1), abort_flag, err);
+        if (!ok) break;
+        // the weight of a NaN key is NaN where it is seen; its V codes are zeros, their scale 0 here
+        convert((v ? sV : sK) + st * S::kKVBytes, sC + cs * S::kCodes, v ? vs & ~nans : ks, v ? 0u : nans,
+                v ? ev : ek, keys, v ? wv : wk);
+        ptx::fence_proxy_async_smem();
+        ptx::mbar_arrive(v ? &bars->v_full[st] : &bars->k_full[st]);
+        ptx::mbar_arrive(&bars->c_empty[cs]);
+      }
+      if (!ok) break;
       cur = nxt;
       nxt = nn;
       pg = pgn;
@@ -869,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // values more than 2^64 below the row's units count as that small (the sum
         // needs the weights above fp32's underflow)
         auto lift = [&]() -> int { return max(ev - evr, -64); };
-        if (!(wide_k || wide_v)) {                    // the same for the whole tile
+        if (__builtin_expect(!(wide_k || wide_v), 1)) {   // the same for the whole tile
           float x[BN];
 #pragma unroll
           for (int cc = 0; cc < BN / 32; ++cc)
