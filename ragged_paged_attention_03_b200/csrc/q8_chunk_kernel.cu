@@ -30,17 +30,18 @@
 // one per CTA; runs that begin or end inside an item leave partial results that
 // combine_kernel joins.
 //
-// Roles (512 threads launched at 128 registers; setmaxnreg: 2 x 128 at 184 and
-// 2 x 128 at 72, together 65,536):
+// Roles (512 threads of at most 128 registers).  Every hot loop is short and
+// rolled: with five kinds of warps on an SM the unrolled forms (a row's 128 scores in
+// registers) were bound by instruction fetch, at a third of this speed.
 //   warps 0-3, 4-7  softmax and output of tile 0 and 1 (one row per thread); they
 //                   also turn their tile's Q, landed by TMA as bf16, into scaled
 //                   fp16 in place
 //   warps 8-11      keys and values: code tiles, landed by TMA, into swizzled fp16 tiles
 //   warp 12         TMEM owner and MMA issue
-//   warp 13, 14     TMA of Q, of the code tiles
-//   warp 15         walks the run and writes its segments down for the others (it waits
-//                   for nothing but their slots: the converters look two blocks ahead,
-//                   into segments whose Q cannot be loaded yet)
+//   warp 13         TMA of Q
+//   warp 14         TMA of the code tiles; the scales of their keys as fp16 factors
+//   warp 15         walks the run and writes its segments down for the others; it waits
+//                   for nothing but their slots
 // TMEM (512 columns): S/P of tile 0 | S/P of tile 1 | O of tile 0 | O of tile 1.
 #include <cuda.h>
 #include <math.h>
@@ -65,7 +66,7 @@ constexpr int kBase = 5;
 constexpr int kWide = 15;           // a tile whose scales spread further is "wide"
 constexpr int kWideBit = 1 << 16;   // in the published ekb / evb
 constexpr int kExpSlots = 8;
-constexpr int kSegSlots = 8;
+constexpr int kSegSlots = 4;
 
 template <int D>
 struct Shape {
@@ -76,7 +77,7 @@ struct Shape {
   static constexpr int kKVBytes = kHalves * BN * 128;
   static constexpr int kCodes = BN * D;
   static constexpr int kData = 2 * kQBytes + (NSK + NSV) * kKVBytes + NST * kCodes;
-  static constexpr int kSmem = 1024 + kData + 1536;
+  static constexpr int kSmem = 1024 + kData + 2048;
   static constexpr uint32_t kTmemCols = 512, kColO = 256;
 };
 
@@ -84,6 +85,7 @@ struct Bars {
   uint64_t q_full[2], q_empty[2], qc_full[2];
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
   uint64_t c_full[4], c_empty[4];
+  uint64_t f_full[2], f_empty[2];
   uint64_t e_full[kExpSlots];
   uint64_t s_full[2], p_full[2], p_half[2], pv_done[2], o_free[2];
   uint64_t seg_full[kSegSlots], seg_empty[kSegSlots];
@@ -101,6 +103,8 @@ struct Seg {
   int32_t pad[2];
 };
 constexpr int kSegUsers = 1 + 2 + 4 + 8;   // warps that release a slot: MMA, TMA, converters, softmax
+
+static_assert(1024 + sizeof(Bars) + 20 * 8 + 2 * kExpSlots * 4 + kSegSlots * sizeof(Seg) + 8 <= 2048, "control block");
 
 struct PartHead {
   int32_t seq, hk, item, begin;
@@ -259,7 +263,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *sK = sQ + 2 * S::kQBytes;
   uint8_t *sV = sK + NSK * S::kKVBytes;
   uint8_t *sC = sV + NSV * S::kKVBytes;
-  Bars *bars = reinterpret_cast<Bars *>(base + S::kData);
+  uint16_t *s_fac = reinterpret_cast<uint16_t *>(base + S::kData);   // [2][K, V][128] factors of a block's keys
+  Bars *bars = reinterpret_cast<Bars *>(s_fac + 2 * 2 * BN);
   int64_t *s_scan = reinterpret_cast<int64_t *>(bars + 1);       // [16 + 4]
   int *s_exp = reinterpret_cast<int *>(s_scan + 20);             // [kExpSlots][2]
   Seg *s_seg = reinterpret_cast<Seg *>(s_exp + 2 * kExpSlots);   // [kSegSlots]
@@ -361,6 +366,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&bars->c_full[i], 1);
       ptx::mbar_init(&bars->c_empty[i], 128);
     }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&bars->f_full[i], 1);
+      ptx::mbar_init(&bars->f_empty[i], 4);
+    }
     for (int i = 0; i < kExpSlots; ++i) ptx::mbar_init(&bars->e_full[i], 1);
     for (int i = 0; i < kSegSlots; ++i) {
       ptx::mbar_init(&bars->seg_full[i], 1);
@@ -398,7 +407,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp >= 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
     if (warp == 15) {
       // ------------------------------------------------------- the run
       Run run;
@@ -456,53 +464,107 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (uses1 > 0) ptx::mbar_wait(&bars->q_full[1], (uint32_t)((uses1 - 1) & 1));
       __syncwarp();
     } else if (warp == 14) {
-      // ------------------------------------------------- TMA of the codes
+      // ----------------------------------- TMA of the codes, the scales
       const int br = a.p < BN ? a.p : BN;
       const int nload = BN / br;
       constexpr int W = D < 128 ? D : 128;
-      int use = 0;                       // code tiles queued
+      int gb = 0;
       bool ok = true;
+      auto queue = [&](int v, bool load, uint32_t bytes, int hk, int row) -> bool {
+        const int use = 2 * gb + v, st = use % S::NST;
+        if (use >= S::NST && !wait_warp(&bars->c_empty[st], (uint32_t)(((use / S::NST) & 1) ^ 1), abort_flag, err))
+          return false;
+        ptx::mbar_arrive_expect_tx_elect(&bars->c_full[st], bytes);
+        __syncwarp();
+        if (load) ptx::tma_load_3d(sC + st * S::kCodes + lane * br * W, v ? &tm_v : &tm_k, &bars->c_full[st], 0, hk, row);
+        __syncwarp();
+        return true;
+      };
+      int queued = 0;                    // code tiles
       while (ok) {
         const Seg *sg = next_seg();
         if (sg == nullptr) break;
         const int blocks = sg->blocks, b0 = sg->b0, kv = sg->kv, hk = sg->hk;
         const int32_t *pt = a.page_table + (size_t)sg->seq * a.max_pages;
         done_seg();
-        auto page_of = [&](int j) -> int {
-          const int pos = (b0 + j) * BN + lane * br;
-          return lane < nload && j < blocks && pos < kv ? pt[pos >> a.p_shift] : -1;
+        // pages as the table has them: of the box this lane queues, and of the lane's
+        // keys 4 lane .. + 3 (-1: no key)
+        auto page_at = [&](int j, int pos, bool use) -> int { return use && j < blocks && pos < kv ? pt[pos >> a.p_shift] : -1; };
+        auto box_page = [&](int j) -> int { return page_at(j, (b0 + j) * BN + lane * br, lane < nload); };
+        auto key_page = [&](int j) -> int { return page_at(j, (b0 + j) * BN + lane * 4, true); };
+        auto scales_of = [&](int j, int pg, const uint8_t *src) -> uint32_t {
+          if ((unsigned)pg >= (unsigned)a.num_pages) return 0;
+          const int pos = (b0 + j) * BN + lane * 4;
+          return *reinterpret_cast<const uint32_t *>(src + ((size_t)pg * a.hkv + hk) * a.p + (pos & (a.p - 1)));
         };
-        int next_page = page_of(0);
-        for (int j = 0; ok && j < blocks; ++j) {
-          const int page = next_page;
-          next_page = page_of(j + 1);
+        int box_next = box_page(0), pg = key_page(0);
+        uint32_t ks = scales_of(0, pg, a.c.ks), vs = scales_of(0, pg, a.c.vs);
+        for (int j = 0; ok && j < blocks; ++j, ++gb) {
+          const int page = box_next;
+          box_next = box_page(j + 1);
+          const int pgn = key_page(j + 1);
           const int pos = (b0 + j) * BN + lane * br;
           const bool load = lane < nload && pos < kv;
           int row = page * a.p + (pos & (a.p - 1));
-          if (load && (page < 0 || page >= a.num_pages)) {
+          if (load && (unsigned)page >= (unsigned)a.num_pages) {
             raise(err, RPA_DEV_BAD_PAGE);
             row = a.num_pages * a.p;       // outside the tensor: the copy fills zeros
           }
           const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, load)) * (uint32_t)(br * D);
+          ok = queue(0, load, bytes, hk, row);
+          if (!ok) break;
+          ++queued;
+          // the block's largest and smallest scales over the keys it has; NaN scales mark the key
+          uint32_t nans = 0;
+          int ek = 0, ev = 0, ek0 = 255, ev0 = 255;
 #pragma unroll
-          for (int kv2 = 0; kv2 < 2; ++kv2, ++use) {
-            const int st = use % S::NST;
-            if (use >= S::NST &&
-                !wait_warp(&bars->c_empty[st], (uint32_t)(((use / S::NST) & 1) ^ 1), abort_flag, err)) {
-              ok = false;
-              break;
-            }
-            ptx::mbar_arrive_expect_tx_elect(&bars->c_full[st], bytes);
-            __syncwarp();
-            if (load)
-              ptx::tma_load_3d(sC + st * S::kCodes + lane * br * W, kv2 ? &tm_v : &tm_k, &bars->c_full[st], 0, hk, row);
-            __syncwarp();
+          for (int k = 0; k < 4; ++k) {
+            const bool key = (unsigned)pg < (unsigned)a.num_pages && (b0 + j) * BN + lane * 4 + k < kv;
+            const int k8 = (ks >> (8 * k)) & 255u, v8 = (vs >> (8 * k)) & 255u;
+            if (key && (k8 == (int)kScaleNan || v8 == (int)kScaleNan)) nans |= 1u << k;
+            if (key && k8 != (int)kScaleNan) ek = max(ek, k8), ek0 = min(ek0, k8);
+            if (key && v8 != (int)kScaleNan) ev = max(ev, v8), ev0 = min(ev0, v8);
           }
+          ek = __reduce_max_sync(0xffffffffu, ek);
+          ev = __reduce_max_sync(0xffffffffu, ev);
+          const bool wk = ek - __reduce_min_sync(0xffffffffu, ek0) > kWide;
+          const bool wv = ev - __reduce_min_sync(0xffffffffu, ev0) > kWide;
+          const int fs = gb & 1;
+          if (gb >= 2) ok = wait_warp(&bars->f_empty[fs], (uint32_t)(((gb >> 1) & 1) ^ 1), abort_flag, err);
+          if (!ok) break;
+          uint32_t fk[4], fv[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const bool nan = (nans >> k) & 1;
+            fk[k] = half_factor(wk ? ek : (int)((ks >> (8 * k)) & 255u), ek, nan);
+            // a NaN key's weight is NaN where it is seen; its values count as zeros elsewhere
+            fv[k] = nan ? 0u : half_factor(wv ? ev : (int)((vs >> (8 * k)) & 255u), ev, false);
+          }
+          uint2 *dst = reinterpret_cast<uint2 *>(s_fac + fs * 2 * BN) + lane;
+          dst[0] = make_uint2(fk[0] | (fk[1] << 16), fk[2] | (fk[3] << 16));
+          dst[BN / 4] = make_uint2(fv[0] | (fv[1] << 16), fv[2] | (fv[3] << 16));
+          if (lane == 0) {
+            // free: the K tile of block gb - 1 is converted, so QK of block gb - 5 or a later one
+            // is done for both tiles, and was issued behind the P of every block before it
+            s_exp[(gb % kExpSlots) * 2] = ek | (wk ? kWideBit : 0);
+            s_exp[(gb % kExpSlots) * 2 + 1] = ev | (wv ? kWideBit : 0);
+          }
+          __syncwarp();
+          if (lane == 0) {
+            ptx::mbar_arrive(&bars->f_full[fs]);
+            ptx::mbar_arrive(&bars->e_full[gb % kExpSlots]);
+          }
+          ok = queue(1, load, bytes, hk, row);
+          if (!ok) break;
+          ++queued;
+          pg = pgn;
+          ks = scales_of(j + 1, pg, a.c.ks);
+          vs = scales_of(j + 1, pg, a.c.vs);
         }
       }
       // queued copies land before the CTA ends
       if (lane == 0)
-        for (int k = use - S::NST < 0 ? 0 : use - S::NST; k < use; ++k)
+        for (int k = queued - S::NST < 0 ? 0 : queued - S::NST; k < queued; ++k)
           ptx::mbar_wait(&bars->c_full[k % S::NST], (uint32_t)((k / S::NST) & 1));
       __syncwarp();
     } else if (warp == 12) {
@@ -582,142 +644,79 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
   } else if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
     // ------------------------------------------------- keys and values
-    constexpr int LPR = D / 16;            // lanes of a row, 16 codes each
-    constexpr int RU = 32 / LPR;           // rows of one load instruction
-    constexpr int NU = BN / RU / 4;        // loads per thread and tile (4 warps)
-    const int cw = warp - 8;
-    const int lrow = lane / LPR, lcol = lane % LPR;
-    // one block ahead of time: which page and scales lane `lane`'s keys (4 lane .. + 3) have
-    struct Block {
-      const int32_t *pt;
-      int hk, kv, b;                       // b < 0: past the run
-    };
-    int seg_left = 0;
-    Block cursor{nullptr, 0, 0, -1};
-    auto advance = [&]() -> Block {
-      while (seg_left == 0) {
-        const Seg *sg = next_seg();
-        if (sg == nullptr) return Block{nullptr, 0, 0, -1};
-        seg_left = sg->blocks;
-        cursor = Block{a.page_table + (size_t)sg->seq * a.max_pages, sg->hk, sg->kv, sg->b0};
-        done_seg();
-      }
-      --seg_left;
-      const Block c = cursor;
-      ++cursor.b;
-      return c;
-    };
-    // the page of the lane's keys as the table has it (checked when it is used, so
-    // that nothing waits for the load), -1: no key
-    auto page_of = [&](const Block &c) -> int {
-      const int pos = c.b * BN + lane * 4;
-      return c.b < 0 || pos >= c.kv ? -1 : c.pt[pos >> a.p_shift];
-    };
-    auto readable = [&](int pg) -> bool { return (unsigned)pg < (unsigned)a.num_pages; };
-    auto scales_of = [&](const Block &c, int pg, const uint8_t *src) -> uint32_t {
-      if (!readable(pg)) return 0;
-      const int pos = c.b * BN + lane * 4;
-      return *reinterpret_cast<const uint32_t *>(src + ((size_t)pg * a.hkv + c.hk) * a.p + (pos & (a.p - 1)));
-    };
-    // what each lane's part of a row goes through: rows differ by their key's factor
-    const uint32_t dup = lrow & 1 ? 0x3232u : 0x1010u;
-    const int c0 = 2 * (lcol & 3), swp = (lcol >> 2) & 1;
-    // code tile -> fp16 tile, key by key times 2^(scale - top); rows from `keys` on, which
-    // no copy filled, become zeros
-    auto convert = [&](uint8_t *dst, const uint8_t *src, uint32_t scales, uint32_t nans, int top, int keys,
-                       bool wide) {
-      // the factors of keys 4 lane .. + 3
-      uint32_t f01, f23;
-      {
-        uint32_t h[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          h[k] = half_factor(wide ? top : (int)((scales >> (8 * k)) & 255u), top, ((nans >> (8 * k)) & 255u) != 0);
-        f01 = h[0] | (h[1] << 16);
-        f23 = h[2] | (h[3] << 16);
-      }
-#pragma unroll 2
-      for (int i = 0; i < NU; ++i) {
-        const int row = (i * 4 + cw) * RU + lrow;
-        uint4 x = *reinterpret_cast<const uint4 *>(src + row * D + lcol * 16);
-        const uint32_t a01 = __shfl_sync(0xffffffffu, f01, row >> 2), a23 = __shfl_sync(0xffffffffu, f23, row >> 2);
-        const uint32_t f = __byte_perm(row & 2 ? a23 : a01, 0u, dup);
-        if (row >= keys) x = make_uint4(0, 0, 0, 0);
-        const uint4 u0 = make_uint4(mul_h2(codes_h2(x.x), f), mul_h2(codes_h2(x.x >> 16), f),
-                                    mul_h2(codes_h2(x.y), f), mul_h2(codes_h2(x.y >> 16), f));
-        const uint4 u1 = make_uint4(mul_h2(codes_h2(x.z), f), mul_h2(codes_h2(x.z >> 16), f),
-                                    mul_h2(codes_h2(x.w), f), mul_h2(codes_h2(x.w >> 16), f));
-        // values 16 lcol .. + 15: chunks c0, c0 + 1 of column tile lcol / 4; lanes of odd
-        // column tiles store theirs in the other order (no bank is hit twice)
-        uint8_t *p = dst + (lcol >> 2) * BN * 128 + row * 128;
-        *reinterpret_cast<uint4 *>(p + (((c0 + swp) ^ (row & 7)) << 4)) = swp ? u1 : u0;
-        *reinterpret_cast<uint4 *>(p + (((c0 + 1 - swp) ^ (row & 7)) << 4)) = swp ? u0 : u1;
-      }
-    };
-    Block cur = advance(), nxt = advance();
-    int pg = page_of(cur), pgn = page_of(nxt);
-    uint32_t ks = scales_of(cur, pg, a.c.ks), vs = scales_of(cur, pg, a.c.vs);
-    for (int gb = 0; cur.b >= 0; ++gb) {
-      const Block nn = advance();
-      const int pgnn = page_of(nn);
-      const uint32_t ksn = scales_of(nxt, pgn, a.c.ks), vsn = scales_of(nxt, pgn, a.c.vs);
-      // this block's largest scales over the keys it has; NaN scales mark the key
-      uint32_t nans = 0;
-      int ek = 0, ev = 0, ek0 = 255, ev0 = 255;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bool key = readable(pg) && cur.b * BN + lane * 4 + j < cur.kv;
-        const uint32_t k8 = (ks >> (8 * j)) & 255u, v8 = (vs >> (8 * j)) & 255u;
-        if (key && (k8 == kScaleNan || v8 == kScaleNan)) nans |= 255u << (8 * j);
-        if (key && k8 != kScaleNan) {
-          ek = max(ek, (int)k8);
-          ek0 = min(ek0, (int)k8);
-        }
-        if (key && v8 != kScaleNan) {
-          ev = max(ev, (int)v8);
-          ev0 = min(ev0, (int)v8);
-        }
-      }
-      ek = __reduce_max_sync(0xffffffffu, ek);
-      ev = __reduce_max_sync(0xffffffffu, ev);
-      const bool wk = ek - __reduce_min_sync(0xffffffffu, ek0) > kWide;
-      const bool wv = ev - __reduce_min_sync(0xffffffffu, ev0) > kWide;
-      const int keys = cur.kv - cur.b * BN;
-      const uint32_t ph = (uint32_t)(((gb / NSK) & 1) ^ 1);
-      bool ok = true;
-#pragma unroll 1
-      for (int v = 0; ok && v < 2; ++v) {
-        const int st = gb % NSK, use = 2 * gb + v, cs = use % S::NST;
-        ok = gb < NSK || wait_warp(v ? &bars->v_empty[st] : &bars->k_empty[st], ph, abort_flag, err);
-        if (ok && v == 0 && warp == 8 && lane == 0) {
-          // free: QK of block gb - 4 or a later one is done for both tiles, and was issued
-          // behind the P of every block up to gb - 5
-          s_exp[(gb % kExpSlots) * 2] = ek | (wk ? kWideBit : 0);
-          s_exp[(gb % kExpSlots) * 2 + 1] = ev | (wv ? kWideBit : 0);
-          ptx::mbar_arrive(&bars->e_full[gb % kExpSlots]);
-        }
-        ok = ok && wait_warp(&bars->c_full[cs], (uint32_t)((use / S::NST) & 1), abort_flag, err);
+    // D / 16 lanes share a row, 16 codes each; a lane's NU rows are neighbours, so their
+    // factors are one load
+    constexpr int LPR = D / 16, NU = BN / (32 / LPR) / 4;
+    const int cw = warp - 8, lrow = lane / LPR, lcol = lane % LPR;
+    const int row0 = lrow * (4 * NU) + cw * NU;
+    // the two 16-byte chunks of a lane's values, in the order that hits no bank twice
+    const int swp = D == 64 ? lrow & 1 : lcol >> 2;
+    const int c0 = 2 * (lcol & 3) + swp, c1 = c0 ^ 1;
+    const uint32_t src0 = (uint32_t)(row0 * D + lcol * 16 + swp * 8);
+    const uint32_t dst0 = (uint32_t)((lcol >> 2) * BN * 128 + row0 * 128);
+    const int x0 = c0 ^ (row0 & 7), x1 = c1 ^ (row0 & 7);      // NU rows from row0 on: row & 7 = (row0 & 7) | i
+    int gb = 0;
+    bool ok = true;
+    while (ok) {
+      const Seg *sg = next_seg();
+      if (sg == nullptr) break;
+      const int blocks = sg->blocks;
+      int keys = sg->kv - sg->b0 * BN;
+      done_seg();
+      for (int j = 0; ok && j < blocks; ++j, ++gb, keys -= BN) {
+        ok = wait_warp(&bars->f_full[gb & 1], (uint32_t)((gb >> 1) & 1), abort_flag, err);
         if (!ok) break;
-        // the weight of a NaN key is NaN where it is seen; its V codes are zeros, their scale 0 here
-        convert((v ? sV : sK) + st * S::kKVBytes, sC + cs * S::kCodes, v ? vs & ~nans : ks, v ? 0u : nans,
-                v ? ev : ek, keys, v ? wv : wk);
-        ptx::fence_proxy_async_smem();
-        ptx::mbar_arrive(v ? &bars->v_full[st] : &bars->k_full[st]);
-        ptx::mbar_arrive(&bars->c_empty[cs]);
+        const int st = gb % NSK;
+#pragma unroll 1
+        for (int v = 0; v < 2; ++v) {
+          const int use = 2 * gb + v, cs = use % S::NST;
+          uint32_t fac[NU / 2];
+          {
+            const uint16_t *fp = s_fac + (gb & 1) * 2 * BN + v * BN + row0;
+            if constexpr (NU == 8) {
+              const uint4 q = *reinterpret_cast<const uint4 *>(fp);
+              fac[0] = q.x; fac[1] = q.y; fac[2] = q.z; fac[3] = q.w;
+            } else {
+              const uint2 q = *reinterpret_cast<const uint2 *>(fp);
+              fac[0] = q.x; fac[1] = q.y;
+            }
+          }
+          ok = gb < NSK || wait_warp(v ? &bars->v_empty[st] : &bars->k_empty[st], (uint32_t)(((gb / NSK) & 1) ^ 1),
+                                     abort_flag, err);
+          ok = ok && wait_warp(&bars->c_full[cs], (uint32_t)((use / S::NST) & 1), abort_flag, err);
+          if (!ok) break;
+          const uint8_t *src = sC + cs * S::kCodes + src0;
+          uint8_t *dst = (v ? sV : sK) + st * S::kKVBytes + dst0;
+#pragma unroll
+          for (int i = 0; i < NU; ++i) {
+            uint2 a0 = *reinterpret_cast<const uint2 *>(src + i * D);
+            uint2 a1 = *reinterpret_cast<const uint2 *>(src + i * D + (swp ? -8 : 8));
+            const uint32_t f = __byte_perm(fac[i / 2], 0u, i & 1 ? 0x3232 : 0x1010);
+            *reinterpret_cast<uint4 *>(dst + i * 128 + ((x0 ^ i) << 4)) =
+                make_uint4(mul_h2(codes_h2(a0.x), f), mul_h2(codes_h2(a0.x >> 16), f),
+                           mul_h2(codes_h2(a0.y), f), mul_h2(codes_h2(a0.y >> 16), f));
+            *reinterpret_cast<uint4 *>(dst + i * 128 + ((x1 ^ i) << 4)) =
+                make_uint4(mul_h2(codes_h2(a1.x), f), mul_h2(codes_h2(a1.x >> 16), f),
+                           mul_h2(codes_h2(a1.y), f), mul_h2(codes_h2(a1.y >> 16), f));
+          }
+          // rows without a key, which no copy filled or whose page holds anything: zeros
+          if (keys < BN)
+#pragma unroll 1
+            for (int i = 0; i < NU; ++i)
+              if (row0 + i >= keys) {
+                *reinterpret_cast<uint4 *>(dst + i * 128 + ((x0 ^ i) << 4)) = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4 *>(dst + i * 128 + ((x1 ^ i) << 4)) = make_uint4(0, 0, 0, 0);
+              }
+          ptx::fence_proxy_async_smem();
+          ptx::mbar_arrive(v ? &bars->v_full[st] : &bars->k_full[st]);
+          ptx::mbar_arrive(&bars->c_empty[cs]);
+        }
+        if (lane == 0) ptx::mbar_arrive(&bars->f_empty[gb & 1]);
       }
-      if (!ok) break;
-      cur = nxt;
-      nxt = nn;
-      pg = pgn;
-      pgn = pgnn;
-      ks = ksn;
-      vs = vsn;
     }
   } else {
     // ------------------------------------------------------ softmax, output
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;" ::: "memory");
     const int t = warp >> 2, row = tid & 127;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t tS = lane_base + (uint32_t)(t * 128);
@@ -756,9 +755,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       {
         uint8_t *q = sQ + t * S::kQBytes + row * 128;
         uint32_t amax = 0;
-#pragma unroll
+#pragma unroll 1
         for (int h = 0; h < S::kHalves; ++h)
-#pragma unroll
+#pragma unroll 4
           for (int c = 0; c < 8; ++c) {
             const uint4 u = *reinterpret_cast<const uint4 *>(q + h * BM * 128 + ((c ^ (row & 7)) << 4));
             const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -768,9 +767,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t code = scale_code(amax);
         const float inv = code == kScaleNan ? 0.f : inverse_scale(code);
         qf = scale_value(code) * f;
-#pragma unroll
+#pragma unroll 1
         for (int h = 0; h < S::kHalves; ++h)
-#pragma unroll
+#pragma unroll 2
           for (int c = 0; c < 8; ++c) {
             uint4 *p = reinterpret_cast<uint4 *>(q + h * BM * 128 + ((c ^ (row & 7)) << 4));
             const uint4 u = *p;
@@ -851,24 +850,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         // needs the weights above fp32's underflow)
         auto lift = [&]() -> int { return max(ev - evr, -64); };
         if (__builtin_expect(!(wide_k || wide_v), 1)) {   // the same for the whole tile
-          float x[BN];
+          // the scores stay in TMEM; 32 of them are in registers, the next 32 in flight
+          const bool masked = __any_sync(0xffffffffu, lim < BN);
+          uint32_t xa[32], xb[32];
+          float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          auto max_of = [&](uint32_t (&x)[32], int c) {
+            if (masked) {
 #pragma unroll
-          for (int cc = 0; cc < BN / 32; ++cc)
-            ptx::tmem_ld32(tS + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[cc * 32]));
-          ptx::tmem_ld_wait();
-          if (__any_sync(0xffffffffu, lim < BN)) {
-#pragma unroll
-            for (int i = 0; i < BN; ++i) x[i] = i < lim ? x[i] : -INFINITY;
-          }
-          float mq[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-          for (int i = 4; i < BN; i += 8) {
-            mq[0] = ptx::fmax3(mq[0], x[i], x[i + 1]);
-            mq[1] = ptx::fmax3(mq[1], x[i + 2], x[i + 3]);
-            if (i + 4 < BN) {
-              mq[2] = ptx::fmax3(mq[2], x[i + 4], x[i + 5]);
-              mq[3] = ptx::fmax3(mq[3], x[i + 6], x[i + 7]);
+              for (int i = 0; i < 32; ++i) x[i] = c + i < lim ? x[i] : 0xff800000u;
             }
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                mq[q] = ptx::fmax3(mq[q], __uint_as_float(x[i + 2 * q]), __uint_as_float(x[i + 2 * q + 1]));
+          };
+          ptx::tmem_ld32(tS, xa);
+          ptx::tmem_ld_wait_for(xa);
+#pragma unroll 1
+          for (int c = 0; c < BN; c += 64) {
+            ptx::tmem_ld32(tS + c + 32, xb);
+            max_of(xa, c);
+            ptx::tmem_ld_wait_for(xb);
+            ptx::tmem_ld32(tS + ((c + 64) & (BN - 1)), xa);      // the last one: the first again
+            max_of(xb, c + 32);
+            ptx::tmem_ld_wait_for(xa);
           }
           const float mx = ptx::fmax3(mq[0], mq[1], fmaxf(mq[2], mq[3])) * sc;
           take_max(mx, mx);
@@ -877,20 +883,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t scale2 = ptx::f2_pack(sc, sc);
           const uint64_t shift2 = ptx::f2_pack(shift, shift);
           uint64_t sp2[4] = {0, 0, 0, 0};
-          uint32_t pk[BN / 2];
+          // P of keys c .. c + 31 into the columns of scores that have been read
+          auto weights_of = [&](uint32_t (&x)[32], int c) {
+            if (masked) {
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
+              for (int i = 0; i < 32; ++i) x[i] = c + i < lim ? x[i] : 0xff800000u;
+            }
+            uint32_t pk[16];
 #pragma unroll
-            for (int i = hf * (BN / 2); i < (hf + 1) * (BN / 2); i += 2) {
+            for (int i = 0; i < 32; i += 2) {
               float a0, a1;
-              ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(x[i], x[i + 1]), scale2, shift2), a0, a1);
+              ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), scale2, shift2),
+                             a0, a1);
               const float p0 = ptx::ex2(a0), p1 = ptx::ex2(a1);
               sp2[(i >> 1) & 3] = ptx::f2_add(sp2[(i >> 1) & 3], ptx::f2_pack(p0, p1));
               pk[i >> 1] = ptx::pack_f16(p0, p1);
             }
-            ptx::tmem_st32(tS + hf * 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[hf * 32]));
-            if (hf == 0) {
-              ptx::tmem_st_wait();
+            ptx::tmem_st16(tS + c / 2, pk);
+          };
+#pragma unroll 1
+          for (int c = 0; c < BN; c += 64) {
+            ptx::tmem_ld32(tS + c + 32, xb);
+            weights_of(xa, c);
+            ptx::tmem_ld_wait_for(xb);
+            if (c == 0) ptx::tmem_ld32(tS + 64, xa);
+            weights_of(xb, c + 32);
+            ptx::tmem_st_wait();
+            if (c == 0) {
+              ptx::tmem_ld_wait_for(xa);
               ptx::tc_fence_before();
               ptx::mbar_arrive(&bars->p_half[t]);
             }
@@ -949,46 +969,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       ptx::tc_fence_after();
-      uint32_t ov[D];
-#pragma unroll
-      for (int cc = 0; cc < D / 32; ++cc)
-        ptx::tmem_ld32(tO + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&ov[cc * 32]));
-      ptx::tmem_ld_wait();
-      ptx::tc_fence_before();
-      ptx::mbar_arrive(&bars->o_free[t]);
       ++ep;
-      const float unit = ptx::ex2((float)(evr - 127));  // O / l is in units of this
       if (end == 0) {                                 // sees no key, whatever its q holds
         l = 0.f;
         m = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < D; ++i) ov[i] = 0;
       }
-      if (mine) {
-        if (whole) {
-          const float inv = l == 0.f ? 0.f : unit / l;
-          __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + at * D;
-          const uint64_t once = ptx::l2_evict_first_policy();
+      // O / l is in units of 2^(evr - 127); a part keeps O in them
+      const float unit = ptx::ex2((float)(evr - 127));
+      const float mul = end == 0 ? 0.f : !whole ? unit : l == 0.f ? 0.f : unit / l;
+      const uint64_t once = ptx::l2_evict_first_policy();
+#pragma unroll 1
+      for (int cc = 0; cc < D; cc += 32) {
+        uint32_t ov[32];
+        ptx::tmem_ld32(tO + cc, ov);
+        ptx::tmem_ld_wait();
+        if (cc + 32 == D) {
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(&bars->o_free[t]);
+        }
+        if (!mine) continue;
 #pragma unroll
-          for (int cc = 0; cc < D / 8; ++cc) {
+        for (int i = 0; i < 32; ++i) ov[i] = end == 0 ? 0u : __float_as_uint(__uint_as_float(ov[i]) * mul);
+        if (whole) {
+          uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + at * D + cc);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
             uint32_t o2[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              o2[i] = ptx::pack_bf16(__uint_as_float(ov[cc * 8 + 2 * i]) * inv,
-                                     __uint_as_float(ov[cc * 8 + 2 * i + 1]) * inv);
-            ptx::st_global_hint(reinterpret_cast<uint4 *>(out) + cc, make_uint4(o2[0], o2[1], o2[2], o2[3]), once);
+            for (int k = 0; k < 4; ++k)
+              o2[k] = ptx::pack_bf16(__uint_as_float(ov[8 * i + 2 * k]), __uint_as_float(ov[8 * i + 2 * k + 1]));
+            ptx::st_global_hint(out + i, make_uint4(o2[0], o2[1], o2[2], o2[3]), once);
           }
-          if (a.lse != nullptr)
-            a.lse[at] = l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l) - kBase) * kLn2;
         } else {
-          g.ml[slot * 256 + t * 128 + row] = make_float2(m, l);
-          float4 *po = g.o + slot * (D / 4) * 256 + t * 128 + row;
+          float4 *po = g.o + (slot * (D / 4) + cc / 4) * 256 + t * 128 + row;
 #pragma unroll
-          for (int cc = 0; cc < D / 4; ++cc)
-            po[cc * 256] = make_float4(__uint_as_float(ov[cc * 4]) * unit, __uint_as_float(ov[cc * 4 + 1]) * unit,
-                                       __uint_as_float(ov[cc * 4 + 2]) * unit, __uint_as_float(ov[cc * 4 + 3]) * unit);
+          for (int i = 0; i < 8; ++i)
+            po[i * 256] = make_float4(__uint_as_float(ov[4 * i]), __uint_as_float(ov[4 * i + 1]),
+                                      __uint_as_float(ov[4 * i + 2]), __uint_as_float(ov[4 * i + 3]));
         }
       }
+      if (!mine) continue;
+      if (!whole)
+        g.ml[slot * 256 + t * 128 + row] = make_float2(m, l);
+      else if (a.lse != nullptr)
+        a.lse[at] = l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l) - kBase) * kLn2;
     }
   }
   ptx::tc_fence_before();
