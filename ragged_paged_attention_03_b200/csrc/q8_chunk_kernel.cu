@@ -42,7 +42,8 @@
 //   warp 14         TMA of the code tiles; the scales of their keys as fp16 factors
 //   warp 15         walks the run and writes its segments down for the others; it waits
 //                   for nothing but their slots
-// TMEM (512 columns): S/P of tile 0 | S/P of tile 1 | O of tile 0 | O of tile 1.
+// TMEM (512 columns): S/P of tile 0 (two buffers of 64 keys) | of tile 1 | O of
+// tile 0 | O of tile 1.
 #include <cuda.h>
 #include <math.h>
 
@@ -58,7 +59,8 @@ namespace q8 {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int BM = 128, BN = 128;
+constexpr int BM = 128, BN = 128;   // rows of a tile, keys of a block
+constexpr int HN = 64;              // keys of a step: half a block
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 6.0f;    // lazy rescale of O: weights reach 2^(6 + kBase)
@@ -87,7 +89,7 @@ struct Bars {
   uint64_t c_full[4], c_empty[4];
   uint64_t f_full[2], f_empty[2];
   uint64_t e_full[kExpSlots];
-  uint64_t s_full[2], p_full[2], p_half[2], pv_done[2], o_free[2];
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2], o_free[2];   // [tile][S buffer]
   uint64_t seg_full[kSegSlots], seg_empty[kSegSlots];
   uint64_t drain;
 };
@@ -96,7 +98,7 @@ struct Bars {
 struct Seg {
   int32_t seq, hk, item, b0;
   int32_t blocks;                // blocks to run; < 0: the end of the run
-  int32_t nt[2], rows[2];        // blocks and rows of each tile
+  int32_t nt[2], rows[2];        // steps and rows of each tile
   int32_t q0, row0;              // first token of the sequence, of the item within it
   int32_t kv, q_len;
   int32_t whole;                 // the item begins and ends here
@@ -197,7 +199,7 @@ struct Run {
   int64_t left;
   SeqItems w;
   int q0, row0, b0, b1, nb;      // of the current segment: first token of the item, its blocks
-  int nt[2];                     // blocks of the segment that tile t takes part in
+  int nt[2];                     // steps (64 keys) of the segment that tile t takes part in
   int rows[2];                   // rows of tile t
 
   __device__ __forceinline__ void load() {
@@ -226,12 +228,12 @@ struct Run {
     for (int t = 0; t < 2; ++t) {
       const int tok = min(g->tpt, max(0, w.q_len - row0 - t * g->tpt));
       rows[t] = tok * G;
-      const int vis = tok == 0 ? 0 : max(1, (w.end_of(row0 + t * g->tpt + tok) + BN - 1) / BN);
-      nt[t] = max(0, min(b1, vis) - b0);
+      const int vis = tok == 0 ? 0 : max(1, (w.end_of(row0 + t * g->tpt + tok) + HN - 1) / HN);
+      nt[t] = max(0, min(2 * b1, vis) - 2 * b0);
     }
     return true;
   }
-  __device__ __forceinline__ int blocks() const { return max(nt[0], nt[1]); }
+  __device__ __forceinline__ int blocks() const { return (max(nt[0], nt[1]) + 1) >> 1; }
 };
 
 // 2^(e - top) as fp16 bits (0 below fp16's range; a byte of no key may lie above
@@ -350,9 +352,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&bars->q_full[i], 1);
       ptx::mbar_init(&bars->q_empty[i], 1);
       ptx::mbar_init(&bars->qc_full[i], 128);
-      ptx::mbar_init(&bars->s_full[i], 1);
-      ptx::mbar_init(&bars->p_full[i], 128);
-      ptx::mbar_init(&bars->p_half[i], 128);
+      for (int k = 0; k < 2; ++k) {
+        ptx::mbar_init(&bars->s_full[i][k], 1);
+        ptx::mbar_init(&bars->p_full[i][k], 128);
+      }
       ptx::mbar_init(&bars->pv_done[i], 1);
       ptx::mbar_init(&bars->o_free[i], 128);
     }
@@ -569,10 +572,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else if (warp == 12) {
       // ---------------------------------------------------------------- MMA
-      // The tensor pipe sees, per segment, QK0(0) QK1(0) PV0(0) and then for every block j
-      // QK0(j+1) PV1(j) QK1(j+1) PV0(j+1): one tile's softmax runs beside the
-      // other's MMAs.  A QK into a tile's S/P columns follows the PV that reads P
-      // there; MMAs of one thread execute in order.
+      // A tile's scores of step n go to its S buffer n & 1, where P of step n replaces them;
+      // QK(n + 2) follows PV(n) into the same buffer, so a tile's softmax has the scores of
+      // step n + 1 while PV(n) and QK(n + 2) run.  MMAs of one thread execute in order.
       const uint64_t dq0 = ptx::umma_desc_sw128(ptx::smem_u32(sQ), 16, 1024);
       const uint64_t dk0 = ptx::umma_desc_sw128(ptx::smem_u32(sK), 16, 1024);
       const uint64_t dv0 = ptx::umma_desc_sw128(ptx::smem_u32(sV), BN * 128, 1024);
@@ -583,55 +585,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (sg == nullptr) break;
         const int n0 = sg->nt[0], n1 = sg->nt[1], nb = sg->blocks;
         done_seg();
-        // one QK and one PV a turn: turn (j, 0) is QK0(j+1) PV1(j), turn (j, 1) QK1(j+1) PV0(j+1)
 #pragma unroll 1
-        for (int turn = -2; ok && turn < 2 * nb; ++turn) {
-          const int t = turn & 1, u = t ^ 1, kb = (turn >> 1) + 1, vb = kb - u;   // tiles and blocks
-          const int nk = t ? n1 : n0, nv = t ? n0 : n1;
-          if (kb < nk) {
-            const int st = (gb + kb) % NSK;
-            if (kb == 0) ok = wait_warp(&bars->qc_full[t], (uint32_t)((t ? ep[1] : ep[0]) & 1), abort_flag, err);
-            ok = ok && wait_warp(&bars->k_full[st], (uint32_t)(((gb + kb) / NSK) & 1), abort_flag, err);
+        for (int turn = -4; ok && turn < 4 * nb; ++turn) {
+          const int t = turn & 1, vn = turn >> 1, kn = vn + 2;     // tile, steps of its PV and its QK
+          const int nt = t ? n1 : n0, g0 = t ? gt[1] : gt[0], e = t ? ep[1] : ep[0];
+          if (vn >= 0 && vn < nt) {
+            const int st = (gb + (vn >> 1)) % NSV, buf = (g0 + vn) & 1;
+            // O of the tile is overwritten by the segment's first PV: it must have been read
+            if (vn == 0 && e > 0) ok = wait_warp(&bars->o_free[t], (uint32_t)((e - 1) & 1), abort_flag, err);
+            ok = ok && wait_warp(&bars->v_full[st], (uint32_t)(((gb + (vn >> 1)) / NSV) & 1), abort_flag, err) &&
+                 wait_warp(&bars->p_full[t][buf], (uint32_t)(((g0 + vn) >> 1) & 1), abort_flag, err);
             if (!ok) break;
             ptx::tc_fence_after();
-            const uint64_t dq = dq0 + (uint64_t)((t * S::kQBytes) >> 4), dk = dk0 + (uint64_t)((st * S::kKVBytes) >> 4);
-            constexpr uint32_t idesc = ptx::umma_idesc_f16(128, BN, false);
+            constexpr uint32_t idesc = ptx::umma_idesc_f16(128, D, true);
+            const uint32_t tS = tmem + t * 128 + buf * HN, tO = tmem + S::kColO + t * D;
+            const uint64_t dv = dv0 + (uint64_t)((st * S::kKVBytes + (vn & 1) * HN * 128) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < HN / 16; ++kk)
+              ptx::umma_ts_elect(tO, tS + kk * 8, dv + (uint64_t)((kk * 16 * 128) >> 4), idesc,
+                                 vn > 0 || kk > 0 ? 1u : 0u);
+            ptx::umma_commit_elect(&bars->pv_done[t]);
+          }
+          if (t == 1 && vn >= 0 && (vn & 1)) ptx::umma_commit_elect(&bars->v_empty[(gb + (vn >> 1)) % NSV]);
+          if (kn < nt) {
+            const int st = (gb + (kn >> 1)) % NSK, buf = (g0 + kn) & 1;
+            if (kn == 0) ok = wait_warp(&bars->qc_full[t], (uint32_t)(e & 1), abort_flag, err);
+            ok = ok && wait_warp(&bars->k_full[st], (uint32_t)(((gb + (kn >> 1)) / NSK) & 1), abort_flag, err);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            const uint64_t dq = dq0 + (uint64_t)((t * S::kQBytes) >> 4);
+            const uint64_t dk = dk0 + (uint64_t)((st * S::kKVBytes + (kn & 1) * HN * 128) >> 4);
+            constexpr uint32_t idesc = ptx::umma_idesc_f16(128, HN, false);
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
               const uint32_t off = ((ks >> 2) * BM * 128 + (ks & 3) * 32) >> 4;
-              ptx::umma_ss_elect(tmem + t * 128, dq + off, dk + off, idesc, ks > 0 ? 1u : 0u);
+              ptx::umma_ss_elect(tmem + t * 128 + buf * HN, dq + off, dk + off, idesc, ks > 0 ? 1u : 0u);
             }
-            ptx::umma_commit_elect(&bars->s_full[t]);
-            if (kb + 1 == nk) ptx::umma_commit_elect(&bars->q_empty[t]);
+            ptx::umma_commit_elect(&bars->s_full[t][buf]);
+            if (kn + 1 == nt) ptx::umma_commit_elect(&bars->q_empty[t]);
           }
-          if (t == 1 && kb < nb) ptx::umma_commit_elect(&bars->k_empty[(gb + kb) % NSK]);
-          if (vb >= 0 && vb < nv) {
-            const int st = (gb + vb) % NSV;
-            const uint32_t ph = (uint32_t)(((u ? gt[1] : gt[0]) + vb) & 1);
-            const int e = u ? ep[1] : ep[0];
-            // O of the tile is overwritten by the segment's first PV: it must have been read
-            if (vb == 0 && e > 0) ok = wait_warp(&bars->o_free[u], (uint32_t)((e - 1) & 1), abort_flag, err);
-            // P arrives in two halves: keys 0..63 feed the first k-steps
-            ok = ok && wait_warp(&bars->v_full[st], (uint32_t)(((gb + vb) / NSV) & 1), abort_flag, err) &&
-                 wait_warp(&bars->p_half[u], ph, abort_flag, err);
-            if (!ok) break;
-            constexpr uint32_t idesc = ptx::umma_idesc_f16(128, D, true);
-            const uint32_t tS = tmem + u * 128, tO = tmem + S::kColO + u * D;
-            const uint64_t dv = dv0 + (uint64_t)((st * S::kKVBytes) >> 4);
-            ptx::tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < BN / 32; ++kk)
-              ptx::umma_ts_elect(tO, tS + kk * 8, dv + (uint64_t)((kk * 16 * 128) >> 4), idesc,
-                                 vb > 0 || kk > 0 ? 1u : 0u);
-            ok = wait_warp(&bars->p_full[u], ph, abort_flag, err);
-            if (!ok) break;
-            ptx::tc_fence_after();
-#pragma unroll
-            for (int kk = BN / 32; kk < BN / 16; ++kk)
-              ptx::umma_ts_elect(tO, tS + kk * 8, dv + (uint64_t)((kk * 16 * 128) >> 4), idesc, 1u);
-            if (vb + 1 == nv) ptx::umma_commit_elect(&bars->pv_done[u]);
-          }
-          if (t == 0 && vb >= 0) ptx::umma_commit_elect(&bars->v_empty[(gb + vb) % NSV]);   // both PVs are issued
+          if (t == 1 && (kn & 1) && kn < 2 * nb) ptx::umma_commit_elect(&bars->k_empty[(gb + (kn >> 1)) % NSK]);
         }
         gb += nb;
         gt[0] += n0;
@@ -719,7 +712,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------ softmax, output
     const int t = warp >> 2, row = tid & 127;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t tS = lane_base + (uint32_t)(t * 128);
     const uint32_t tO = lane_base + S::kColO + (uint32_t)(t * D);
     const int tok = row / G, head = row - tok * G;
     const float f = a.scale * kLog2e;
@@ -785,19 +777,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float m = -INFINITY, l = 0.f;                   // l counts 2^kBase per unit weight
       int evr = 0;                                    // O is in units of 2^(m + evr - kBase)
-      for (int j = 0; j < nt; ++j) {
-        const int eslot = (gb + j) % kExpSlots;
-        if (!wait_warp(&bars->e_full[eslot], (uint32_t)(((gb + j) / kExpSlots) & 1), abort_flag, err) ||
-            !wait_warp(&bars->s_full[t], (uint32_t)((gt + j) & 1), abort_flag, err)) {
+      for (int j = 0; j < nt; ++j) {                  // steps
+        const int blk = gb + (j >> 1), eslot = blk % kExpSlots, buf = (gt + j) & 1;
+        const uint32_t tS = lane_base + (uint32_t)(t * 128 + buf * HN);
+        if (!wait_warp(&bars->e_full[eslot], (uint32_t)((blk / kExpSlots) & 1), abort_flag, err) ||
+            !wait_warp(&bars->s_full[t][buf], (uint32_t)(((gt + j) >> 1) & 1), abort_flag, err)) {
           ok = false;
           break;
         }
+        const int key0 = b0 * BN + j * HN;            // the step's first key
         const int ek = s_exp[eslot * 2] & 255, ev = s_exp[eslot * 2 + 1] & 255;
         const bool wide_k = s_exp[eslot * 2] >= kWideBit, wide_v = s_exp[eslot * 2 + 1] >= kWideBit;
         // For a wide tile (whose codes carry no scale): the scale byte of key i, -1 if it
         // is not seen or its page is outside the pool
         auto scale_byte = [&](const uint8_t *src, int i) -> int {
-          const int pos = (b0 + j) * BN + i;
+          const int pos = key0 + i;
           const int pg = pos < end ? pt[pos >> a.p_shift] : -1;
           if (pg < 0 || pg >= a.num_pages) return -1;
           return src[((size_t)pg * a.hkv + hk) * a.p + (pos & (a.p - 1))];
@@ -812,18 +806,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           return (float)((wide_v ? scale_byte(a.c.vs, i) : top) - ref);
         };
         ptx::tc_fence_after();
-        const int lim = min(BN, end - (b0 + j) * BN);
+        const int lim = min(HN, end - key0);
         // never 0, which would make NaN of a masked score
         float sc = qf * scale_value((uint32_t)ek);
         if (sc < 1e-37f) sc = 1e-37f;
         // Moves m (and the units of O, evr) to what the block needs: mx its largest score, my
         // its largest score with the V scale, relative to 2^ev.
-        auto take_max = [&](float mx, float my) {
+        auto take_max = [&](float mx, float my) -> bool {
           const float m_new = fmaxf(m, mx);
           // contributions of the row may pass the units of O by 2^kRescale
           const bool need = m_new > m + kRescale || my + (float)(ev - evr) > m + kRescale;
           if (__any_sync(0xffffffffu, need)) {
-            // PV(t, j - 1) is complete: s_full(t, j) was committed after QK(t, j), issued behind it.
+            // O must be complete up to the step before
+            if (j > 0 && !wait_warp(&bars->pv_done[t], (uint32_t)((gt + j - 1) & 1), abort_flag, err)) return false;
+            ptx::tc_fence_after();
             // The new units: the larger of the old ones and the block's largest contribution
             // (a row that has seen nothing has no old ones)
             const float top = m == -INFINITY ? my + (float)ev : fmaxf(m + (float)evr, my + (float)ev);
@@ -845,85 +841,58 @@ __global__ void __launch_bounds__(kThreads, 1)
             m = m_new;
             evr = evn;
           }
+          return true;
         };
         // values more than 2^64 below the row's units count as that small (the sum
         // needs the weights above fp32's underflow)
         auto lift = [&]() -> int { return max(ev - evr, -64); };
         if (__builtin_expect(!(wide_k || wide_v), 1)) {   // the same for the whole tile
-          // the scores stay in TMEM; 32 of them are in registers, the next 32 in flight
-          const bool masked = __any_sync(0xffffffffu, lim < BN);
-          uint32_t xa[32], xb[32];
-          float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          auto max_of = [&](uint32_t (&x)[32], int c) {
-            if (masked) {
+          uint32_t x[HN];
+          ptx::tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+          ptx::tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
+          ptx::tmem_ld_wait();
+          if (__any_sync(0xffffffffu, lim < HN)) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] = c + i < lim ? x[i] : 0xff800000u;
-            }
-#pragma unroll
-            for (int i = 0; i < 32; i += 8)
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                mq[q] = ptx::fmax3(mq[q], __uint_as_float(x[i + 2 * q]), __uint_as_float(x[i + 2 * q + 1]));
-          };
-          ptx::tmem_ld32(tS, xa);
-          ptx::tmem_ld_wait_for(xa);
-#pragma unroll 1
-          for (int c = 0; c < BN; c += 64) {
-            ptx::tmem_ld32(tS + c + 32, xb);
-            max_of(xa, c);
-            ptx::tmem_ld_wait_for(xb);
-            ptx::tmem_ld32(tS + ((c + 64) & (BN - 1)), xa);      // the last one: the first again
-            max_of(xb, c + 32);
-            ptx::tmem_ld_wait_for(xa);
+            for (int i = 0; i < HN; ++i) x[i] = i < lim ? x[i] : 0xff800000u;
           }
+          float mq[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) mq[q] = fmaxf(__uint_as_float(x[2 * q]), __uint_as_float(x[2 * q + 1]));
+#pragma unroll
+          for (int i = 8; i < HN; i += 8)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              mq[q] = ptx::fmax3(mq[q], __uint_as_float(x[i + 2 * q]), __uint_as_float(x[i + 2 * q + 1]));
           const float mx = ptx::fmax3(mq[0], mq[1], fmaxf(mq[2], mq[3])) * sc;
-          take_max(mx, mx);
+          if (!take_max(mx, mx)) {
+            ok = false;
+            break;
+          }
           const int dv = lift();
           const float shift = (m == -INFINITY ? 0.f : -m) + (float)(kBase + dv);
           const uint64_t scale2 = ptx::f2_pack(sc, sc);
           const uint64_t shift2 = ptx::f2_pack(shift, shift);
           uint64_t sp2[4] = {0, 0, 0, 0};
-          // P of keys c .. c + 31 into the columns of scores that have been read
-          auto weights_of = [&](uint32_t (&x)[32], int c) {
-            if (masked) {
+          uint32_t pk[HN / 2];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] = c + i < lim ? x[i] : 0xff800000u;
-            }
-            uint32_t pk[16];
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              float a0, a1;
-              ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), scale2, shift2),
-                             a0, a1);
-              const float p0 = ptx::ex2(a0), p1 = ptx::ex2(a1);
-              sp2[(i >> 1) & 3] = ptx::f2_add(sp2[(i >> 1) & 3], ptx::f2_pack(p0, p1));
-              pk[i >> 1] = ptx::pack_f16(p0, p1);
-            }
-            ptx::tmem_st16(tS + c / 2, pk);
-          };
-#pragma unroll 1
-          for (int c = 0; c < BN; c += 64) {
-            ptx::tmem_ld32(tS + c + 32, xb);
-            weights_of(xa, c);
-            ptx::tmem_ld_wait_for(xb);
-            if (c == 0) ptx::tmem_ld32(tS + 64, xa);
-            weights_of(xb, c + 32);
-            ptx::tmem_st_wait();
-            if (c == 0) {
-              ptx::tmem_ld_wait_for(xa);
-              ptx::tc_fence_before();
-              ptx::mbar_arrive(&bars->p_half[t]);
-            }
+          for (int i = 0; i < HN; i += 2) {
+            float a0, a1;
+            ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), scale2, shift2), a0,
+                           a1);
+            const float p0 = ptx::ex2(a0), p1 = ptx::ex2(a1);
+            sp2[(i >> 1) & 3] = ptx::f2_add(sp2[(i >> 1) & 3], ptx::f2_pack(p0, p1));
+            pk[i >> 1] = ptx::pack_f16(p0, p1);
           }
+          ptx::tmem_st32(tS, pk);
           float sp[8];
 #pragma unroll
           for (int k = 0; k < 4; ++k) ptx::f2_unpack(sp2[k], sp[2 * k], sp[2 * k + 1]);
           const float sum = ((sp[0] + sp[1]) + (sp[2] + sp[3])) + ((sp[4] + sp[5]) + (sp[6] + sp[7]));
-          l += sum * ptx::ex2((float)-dv);            // weights of this block carry 2^dv
+          l += sum * ptx::ex2((float)-dv);            // weights of this step carry 2^dv
         } else {
           float mx = -INFINITY, my = -INFINITY;
 #pragma unroll 1
-          for (int c = 0; c < BN; c += 8) {
+          for (int c = 0; c < HN; c += 8) {
             uint32_t v[8];
             ptx::tmem_ld8(tS + c, v, 0);
             ptx::tmem_ld_wait();
@@ -934,12 +903,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               my = fmaxf(my, y + wide_ev(c + i, ev, ev));
             }
           }
-          take_max(mx, my);
+          if (!take_max(mx, my)) {
+            ok = false;
+            break;
+          }
           // the sum of the bare weights; P with each key's scale
           const float shift = (m == -INFINITY ? 0.f : -m) + (float)kBase;
           float sum = 0.f;
 #pragma unroll 1
-          for (int c = 0; c < BN; c += 8) {
+          for (int c = 0; c < HN; c += 8) {
             uint32_t v[8], pk[4];
             ptx::tmem_ld8(tS + c, v, 0);
             ptx::tmem_ld_wait();
@@ -952,19 +924,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ptx::tmem_st4(tS + c / 2, pk);            // behind what has been read
           }
-          ptx::tmem_st_wait();
-          ptx::tc_fence_before();
-          ptx::mbar_arrive(&bars->p_half[t]);
           l += sum;
         }
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
-        ptx::mbar_arrive(&bars->p_full[t]);
+        ptx::mbar_arrive(&bars->p_full[t][buf]);
       }
       if (!ok) break;
       gb += nb;
       gt += nt;
-      if (!wait_warp(&bars->pv_done[t], (uint32_t)(ep & 1), abort_flag, err)) {
+      // the last PV, behind the one before it: a parity tells neighbouring phases apart only
+      if ((nt > 1 && !wait_warp(&bars->pv_done[t], (uint32_t)((gt - 2) & 1), abort_flag, err)) ||
+          !wait_warp(&bars->pv_done[t], (uint32_t)((gt - 1) & 1), abort_flag, err)) {
         ok = false;
         break;
       }
