@@ -37,11 +37,11 @@
 //                   also turn their tile's Q, landed by TMA as bf16, into scaled
 //                   fp16 in place
 //   warps 8-11      keys and values: code tiles, landed by TMA, into swizzled fp16 tiles
-//   warp 12         TMEM owner and MMA issue
-//   warp 13         TMA of Q
+//   warps 12, 15    MMA issue of tile 0 and 1 (warp 12 owns TMEM).  One warp for both
+//                   took 4,500 clocks for a step of the two tiles, waits that
+//                   were over included, and held everything else up
+//   warp 13         walks the run: writes its segments down for the others; TMA of Q
 //   warp 14         TMA of the code tiles; the scales of their keys as fp16 factors
-//   warp 15         walks the run and writes its segments down for the others; it waits
-//                   for nothing but their slots
 // TMEM (512 columns): S/P of tile 0 (two buffers of 64 keys) | of tile 1 | O of
 // tile 0 | O of tile 1.
 #include <cuda.h>
@@ -91,10 +91,10 @@ struct Bars {
   uint64_t e_full[kExpSlots];
   uint64_t s_full[2][2], p_full[2][2], pv_done[2], o_free[2];   // [tile][S buffer]
   uint64_t seg_full[kSegSlots], seg_empty[kSegSlots];
-  uint64_t drain;
+  uint64_t drain[2];
 };
 
-// One item's part of the CTA's run, written by warp 15 for the others.
+// One item's part of the CTA's run, written by warp 13 for the others.
 struct Seg {
   int32_t seq, hk, item, b0;
   int32_t blocks;                // blocks to run; < 0: the end of the run
@@ -104,7 +104,7 @@ struct Seg {
   int32_t whole;                 // the item begins and ends here
   int32_t pad[2];
 };
-constexpr int kSegUsers = 1 + 2 + 4 + 8;   // warps that release a slot: MMA, TMA, converters, softmax
+constexpr int kSegUsers = 2 + 1 + 4 + 8;   // warps that release a slot: MMA, TMA of codes, converters, softmax
 
 static_assert(1024 + sizeof(Bars) + 20 * 8 + 2 * kExpSlots * 4 + kSegSlots * sizeof(Seg) + 8 <= 2048, "control block");
 
@@ -121,14 +121,16 @@ struct Args {
   float4 *o;             // [2 * ctas][D / 4][256]
 };
 
-// Waits for a phase, for at most kWaitTries polls (a second or more): false, with
-// RPA_DEV_TIMEOUT raised, when they run out or another warp gave up.  Kept short:
-// the kernel's roles share one instruction cache.
-constexpr uint32_t kWaitTries = 1u << 25;
+// Waits for a phase, for at most kWaitLimitNs: false, with RPA_DEV_TIMEOUT raised,
+// when that runs out or another warp gave up.  The clock is looked at every 64 polls.
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort_flag, uint32_t *err) {
   uint32_t n = 0;
+  uint64_t t0 = 0;
   while (!ptx::mbar_try_wait(bar, parity)) {
-    if ((++n & 63) == 0 && (*abort_flag || n >= kWaitTries)) {
+    if ((++n & 63) != 0) continue;
+    const uint64_t now = ptx::globaltimer();
+    if (n == 64) t0 = now;
+    if (*abort_flag || now - t0 > ptx::kWaitLimitNs) {
       *abort_flag = 1;
       raise(err, RPA_DEV_TIMEOUT);
       return false;
@@ -361,9 +363,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 4; ++i) {
       ptx::mbar_init(&bars->k_full[i], 128);
-      ptx::mbar_init(&bars->k_empty[i], 1);
+      ptx::mbar_init(&bars->k_empty[i], 2);
       ptx::mbar_init(&bars->v_full[i], 128);
-      ptx::mbar_init(&bars->v_empty[i], 1);
+      ptx::mbar_init(&bars->v_empty[i], 2);
     }
     for (int i = 0; i < 4; ++i) {
       ptx::mbar_init(&bars->c_full[i], 1);
@@ -378,7 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&bars->seg_full[i], 1);
       ptx::mbar_init(&bars->seg_empty[i], kSegUsers);
     }
-    ptx::mbar_init(&bars->drain, 1);
+    ptx::mbar_init(&bars->drain[0], 1);
+    ptx::mbar_init(&bars->drain[1], 1);
     *abort_flag = 0;
     ptx::fence_barrier_init();
   }
@@ -410,8 +413,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp >= 12) {
-    if (warp == 15) {
-      // ------------------------------------------------------- the run
+    if (warp == 13) {
+      // --------------------------------------------- the run, TMA of Q
       Run run;
       run.g = &g;
       run.n = n;
@@ -421,7 +424,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       run.blk = (int)s_scan[19];
       run.left = count;
       run.load();
-      for (bool more = true; more; ++segs) {
+      const uint64_t once = ptx::l2_evict_first_policy();
+      int uses0 = 0, uses1 = 0;
+      const uint32_t bytes = (uint32_t)(S::kHalves * 128 * g.tpt * G);
+      bool ok = true;
+      for (bool more = true; ok && more; ++segs) {
         const int slot = segs % kSegSlots;
         if (segs >= kSegSlots &&
             !wait_warp(&bars->seg_empty[slot], (uint32_t)(((segs / kSegSlots) & 1) ^ 1), abort_flag, err))
@@ -438,27 +445,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::mbar_arrive(&bars->seg_full[slot]);
         }
         __syncwarp();
-      }
-    } else if (warp == 13) {
-      // ---------------------------------------------------------- TMA of Q
-      const uint64_t once = ptx::l2_evict_first_policy();
-      int uses0 = 0, uses1 = 0;
-      const uint32_t bytes = (uint32_t)(S::kHalves * 128 * g.tpt * G);
-      bool ok = true;
-      while (ok) {
-        const Seg *sg = next_seg();
-        if (sg == nullptr) break;
-        const int n0 = sg->nt[0], n1 = sg->nt[1], h0 = sg->hk * G, tok = sg->q0 + sg->row0;
-        done_seg();
         for (int t = 0; t < 2; ++t) {
-          if (!ok || (t ? n1 : n0) == 0) continue;
+          if (!ok || !more || (t ? run.nt[1] : run.nt[0]) == 0) continue;
           const int u = t ? uses1 : uses0;
           if (u > 0) ok = wait_warp(&bars->q_empty[t], (uint32_t)((u - 1) & 1), abort_flag, err);
           if (!ok) continue;
           ptx::mbar_arrive_expect_tx_elect(&bars->q_full[t], bytes);
           for (int h = 0; h < S::kHalves; ++h)
-            ptx::tma_load_3d_hint_elect(sQ + t * S::kQBytes + h * BM * 128, &tm_q, &bars->q_full[t], h * 64, h0,
-                                        tok + t * g.tpt, once);
+            ptx::tma_load_3d_hint_elect(sQ + t * S::kQBytes + h * BM * 128, &tm_q, &bars->q_full[t], h * 64,
+                                        run.hk * G, run.q0 + run.row0 + t * g.tpt, once);
           if (t) ++uses1; else ++uses0;
         }
       }
@@ -570,70 +565,73 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = queued - S::NST < 0 ? 0 : queued - S::NST; k < queued; ++k)
           ptx::mbar_wait(&bars->c_full[k % S::NST], (uint32_t)((k / S::NST) & 1));
       __syncwarp();
-    } else if (warp == 12) {
-      // ---------------------------------------------------------------- MMA
+    } else {
+      // ------------------------------------------------- MMA of one tile
       // A tile's scores of step n go to its S buffer n & 1, where P of step n replaces them;
       // QK(n + 2) follows PV(n) into the same buffer, so a tile's softmax has the scores of
       // step n + 1 while PV(n) and QK(n + 2) run.  MMAs of one thread execute in order.
-      const uint64_t dq0 = ptx::umma_desc_sw128(ptx::smem_u32(sQ), 16, 1024);
+      const int t = warp == 12 ? 0 : 1;
+      const uint64_t dq = ptx::umma_desc_sw128(ptx::smem_u32(sQ) + t * S::kQBytes, 16, 1024);
       const uint64_t dk0 = ptx::umma_desc_sw128(ptx::smem_u32(sK), 16, 1024);
       const uint64_t dv0 = ptx::umma_desc_sw128(ptx::smem_u32(sV), BN * 128, 1024);
-      int gb = 0, gt[2] = {0, 0}, ep[2] = {0, 0};
+      const uint32_t tS0 = tmem + t * 128, tO = tmem + S::kColO + t * D;
+      constexpr uint32_t idesc_qk = ptx::umma_idesc_f16(128, HN, false), idesc_pv = ptx::umma_idesc_f16(128, D, true);
+      int gb = 0, gt = 0, ep = 0;
       bool ok = true;
       while (ok) {
         const Seg *sg = next_seg();
         if (sg == nullptr) break;
-        const int n0 = sg->nt[0], n1 = sg->nt[1], nb = sg->blocks;
+        const int nt = sg->nt[t], nb = sg->blocks;
         done_seg();
 #pragma unroll 1
-        for (int turn = -4; ok && turn < 4 * nb; ++turn) {
-          const int t = turn & 1, vn = turn >> 1, kn = vn + 2;     // tile, steps of its PV and its QK
-          const int nt = t ? n1 : n0, g0 = t ? gt[1] : gt[0], e = t ? ep[1] : ep[0];
-          if (vn >= 0 && vn < nt) {
-            const int st = (gb + (vn >> 1)) % NSV, buf = (g0 + vn) & 1;
-            // O of the tile is overwritten by the segment's first PV: it must have been read
-            if (vn == 0 && e > 0) ok = wait_warp(&bars->o_free[t], (uint32_t)((e - 1) & 1), abort_flag, err);
-            ok = ok && wait_warp(&bars->v_full[st], (uint32_t)(((gb + (vn >> 1)) / NSV) & 1), abort_flag, err) &&
-                 wait_warp(&bars->p_full[t][buf], (uint32_t)(((g0 + vn) >> 1) & 1), abort_flag, err);
-            if (!ok) break;
-            ptx::tc_fence_after();
-            constexpr uint32_t idesc = ptx::umma_idesc_f16(128, D, true);
-            const uint32_t tS = tmem + t * 128 + buf * HN, tO = tmem + S::kColO + t * D;
-            const uint64_t dv = dv0 + (uint64_t)((st * S::kKVBytes + (vn & 1) * HN * 128) >> 4);
-#pragma unroll
-            for (int kk = 0; kk < HN / 16; ++kk)
-              ptx::umma_ts_elect(tO, tS + kk * 8, dv + (uint64_t)((kk * 16 * 128) >> 4), idesc,
-                                 vn > 0 || kk > 0 ? 1u : 0u);
-            ptx::umma_commit_elect(&bars->pv_done[t]);
-          }
-          if (t == 1 && vn >= 0 && (vn & 1)) ptx::umma_commit_elect(&bars->v_empty[(gb + (vn >> 1)) % NSV]);
-          if (kn < nt) {
-            const int st = (gb + (kn >> 1)) % NSK, buf = (g0 + kn) & 1;
-            if (kn == 0) ok = wait_warp(&bars->qc_full[t], (uint32_t)(e & 1), abort_flag, err);
-            ok = ok && wait_warp(&bars->k_full[st], (uint32_t)(((gb + (kn >> 1)) / NSK) & 1), abort_flag, err);
-            if (!ok) break;
-            ptx::tc_fence_after();
-            const uint64_t dq = dq0 + (uint64_t)((t * S::kQBytes) >> 4);
-            const uint64_t dk = dk0 + (uint64_t)((st * S::kKVBytes + (kn & 1) * HN * 128) >> 4);
-            constexpr uint32_t idesc = ptx::umma_idesc_f16(128, HN, false);
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-              const uint32_t off = ((ks >> 2) * BM * 128 + (ks & 3) * 32) >> 4;
-              ptx::umma_ss_elect(tmem + t * 128 + buf * HN, dq + off, dk + off, idesc, ks > 0 ? 1u : 0u);
+        for (int vn = -2; vn < 2 * nb; ++vn) {
+          const int kn = vn + 2;
+          if (vn >= 0) {
+            // (a block's tiles are waited for, and released, by both warps, whichever tile uses
+            // them: an arrival of one warp must not count for the next block in the slot)
+            const int st = (gb + (vn >> 1)) % NSV;
+            if ((vn & 1) == 0 && !wait_warp(&bars->v_full[st], (uint32_t)(((gb + (vn >> 1)) / NSV) & 1), abort_flag, err)) {
+              ok = false;
+              break;
             }
+            if (vn < nt) {
+              const int buf = (gt + vn) & 1;
+              // O is overwritten by the segment's first PV: it must have been read
+              if (vn == 0 && ep > 0) ok = wait_warp(&bars->o_free[t], (uint32_t)((ep - 1) & 1), abort_flag, err);
+              ok = ok && wait_warp(&bars->p_full[t][buf], (uint32_t)(((gt + vn) >> 1) & 1), abort_flag, err);
+              if (!ok) break;
+              ptx::tc_fence_after();
+              ptx::umma_ts_x4_elect(tO, tS0 + buf * HN, dv0 + (uint64_t)((st * S::kKVBytes + (vn & 1) * HN * 128) >> 4),
+                                    idesc_pv, vn > 0 ? 1u : 0u);
+              ptx::umma_commit_elect(&bars->pv_done[t]);
+            }
+            if (vn & 1) ptx::umma_commit_elect(&bars->v_empty[st]);
+          }
+          const int st = (gb + (kn >> 1)) % NSK;
+          if ((kn & 1) == 0 && kn < 2 * nb) {
+            ok = wait_warp(&bars->k_full[st], (uint32_t)(((gb + (kn >> 1)) / NSK) & 1), abort_flag, err);
+            if (ok && kn == 0 && nt > 0) ok = wait_warp(&bars->qc_full[t], (uint32_t)(ep & 1), abort_flag, err);
+            if (!ok) break;
+            ptx::tc_fence_after();
+          }
+          if (kn < nt) {
+            const int buf = (gt + kn) & 1;
+            const uint64_t dk = dk0 + (uint64_t)((st * S::kKVBytes + (kn & 1) * HN * 128) >> 4);
+#pragma unroll
+            for (int h = 0; h < S::kHalves; ++h)
+              ptx::umma_ss_x4_elect(tS0 + buf * HN, dq + (uint64_t)((h * BM * 128) >> 4),
+                                    dk + (uint64_t)((h * BN * 128) >> 4), idesc_qk, h > 0 ? 1u : 0u);
             ptx::umma_commit_elect(&bars->s_full[t][buf]);
             if (kn + 1 == nt) ptx::umma_commit_elect(&bars->q_empty[t]);
           }
-          if (t == 1 && (kn & 1) && kn < 2 * nb) ptx::umma_commit_elect(&bars->k_empty[(gb + (kn >> 1)) % NSK]);
+          if ((kn & 1) && kn < 2 * nb) ptx::umma_commit_elect(&bars->k_empty[st]);
         }
         gb += nb;
-        gt[0] += n0;
-        gt[1] += n1;
-        ep[0] += n0 > 0 ? 1 : 0;
-        ep[1] += n1 > 0 ? 1 : 0;
+        gt += nt;
+        ep += nt > 0 ? 1 : 0;
       }
-      ptx::umma_commit_elect(&bars->drain);
-      ptx::mbar_wait(&bars->drain, 0);
+      ptx::umma_commit_elect(&bars->drain[t]);
+      ptx::mbar_wait(&bars->drain[t], 0);
       __syncwarp();
     }
   } else if (warp >= 8) {
