@@ -89,7 +89,7 @@ struct Bars {
   uint64_t c_full[4], c_empty[4];
   uint64_t f_full[2], f_empty[2];
   uint64_t e_full[kExpSlots];
-  uint64_t s_full[2][2], p_full[2][2], pv_done[2], o_free[2];   // [tile][S buffer]
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], o_free[2];   // [tile][S buffer]
   uint64_t seg_full[kSegSlots], seg_empty[kSegSlots];
   uint64_t drain[2];
 };
@@ -281,11 +281,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int G = a.hq / a.hkv;
   uint32_t *err = a.err;
 
+  // This kernel may begin while the call's row-group kernels, queued before it, still run.
+  // It reads nothing of theirs (and they began behind everything queued before the call),
+  // but what the stream holds next counts on them: every CTA waits for them as it ends.
+  auto finish = [] { asm volatile("griddepcontrol.wait;" ::: "memory"); };
   // ---- this CTA's run of blocks
   const int n = checked_seqs(a.len);
   if (n < 0) {
     if (cta == 0 && tid == 0) raise(err, RPA_DEV_BAD_LENGTHS);
     if (tid == 0) g.heads[cta].begin = 0;
+    finish();
     return;
   }
   int64_t mine = 0;
@@ -305,6 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t count = per + (cta < extra ? 1 : 0);
   if (count == 0) {
     if (tid == 0) g.heads[cta].begin = 0;
+    finish();
     return;
   }
   int64_t before = 0;
@@ -357,8 +363,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; k < 2; ++k) {
         ptx::mbar_init(&bars->s_full[i][k], 1);
         ptx::mbar_init(&bars->p_full[i][k], 128);
+        ptx::mbar_init(&bars->pv_done[i][k], 1);
       }
-      ptx::mbar_init(&bars->pv_done[i], 1);
       ptx::mbar_init(&bars->o_free[i], 128);
     }
     for (int i = 0; i < 4; ++i) {
@@ -603,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               ptx::tc_fence_after();
               ptx::umma_ts_x4_elect(tO, tS0 + buf * HN, dv0 + (uint64_t)((st * S::kKVBytes + (vn & 1) * HN * 128) >> 4),
                                     idesc_pv, vn > 0 ? 1u : 0u);
-              ptx::umma_commit_elect(&bars->pv_done[t]);
+              ptx::umma_commit_elect(&bars->pv_done[t][buf]);
             }
             if (vn & 1) ptx::umma_commit_elect(&bars->v_empty[st]);
           }
@@ -713,79 +719,100 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tO = lane_base + S::kColO + (uint32_t)(t * D);
     const int tok = row / G, head = row - tok * G;
     const float f = a.scale * kLog2e;
-    int gb = 0, gt = 0, ep = 0;
-    bool ok = true, head_written = false;
-    while (ok) {
+    int gb = 0, gt = 0, eq = 0;                       // blocks, steps and Q tiles so far
+    bool ok = true;
+    // this row's view of a segment
+    struct View {
+      int nt, nb, b0, hk, end;                        // end: keys the row sees
+      bool mine, whole;
+      const int32_t *pt;
+      size_t slot, at;                                // place of a part; the row in out and lse
+      float qf;                                       // score factor of the row
+    };
+    // Takes the next segment and makes scaled fp16 of its Q, landed as bf16, in place
+    // (the row is this thread's); false at the end of the run.
+    auto take = [&](View &c) -> bool {
       const Seg *sg = next_seg();
-      if (sg == nullptr) break;
-      const int nt = sg->nt[t], nb = sg->blocks;
-      const bool mine = row < sg->rows[t];
-      const bool whole = sg->whole != 0;
-      const int b0 = sg->b0, hk = sg->hk;
-      const int32_t *pt = a.page_table + (size_t)sg->seq * a.max_pages;
-      const size_t slot = 2 * (size_t)cta + (b0 > 0 ? 0 : 1);
-      if (!head_written && tid == 0) g.heads[cta] = PartHead{sg->seq, sg->hk, sg->item, b0};
-      head_written = true;
+      if (sg == nullptr) return false;
+      c.nt = sg->nt[t];
+      c.nb = sg->blocks;
+      c.b0 = sg->b0;
+      c.hk = sg->hk;
+      c.mine = row < sg->rows[t];
+      c.whole = sg->whole != 0;
+      c.pt = a.page_table + (size_t)sg->seq * a.max_pages;
+      c.slot = 2 * (size_t)cta + (c.b0 > 0 ? 0 : 1);
+      if (segs == 0 && tid == 0) g.heads[cta] = PartHead{sg->seq, sg->hk, sg->item, sg->b0};
       const int tk = sg->row0 + t * g.tpt + tok;      // token within the sequence
-      const int end = !mine ? 0 : !a.causal ? sg->kv : min(sg->kv, max(0, sg->kv - sg->q_len + tk + 1));
-      const size_t at = (size_t)(sg->q0 + tk) * a.hq + sg->hk * G + head;   // the row in out and lse
+      c.end = !c.mine ? 0 : !a.causal ? sg->kv : min(sg->kv, max(0, sg->kv - sg->q_len + tk + 1));
+      c.at = (size_t)(sg->q0 + tk) * a.hq + sg->hk * G + head;
       done_seg();
-      if (nt == 0) {
+      if (c.nt == 0) return true;
+      if (!wait_warp(&bars->q_full[t], (uint32_t)(eq & 1), abort_flag, err)) {
+        ok = false;
+        return false;
+      }
+      ++eq;
+      uint8_t *q = sQ + t * S::kQBytes + row * 128;
+      uint32_t big = 0;                               // largest |q| of the even and the odd values (NaN stays)
+#pragma unroll 1
+      for (int h = 0; h < S::kHalves; ++h)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 u = *reinterpret_cast<const uint4 *>(q + h * BM * 128 + ((i ^ (row & 7)) << 4));
+          big = ptx::absmax_bf16x2(ptx::absmax_bf16x2(big, u.x), ptx::absmax_bf16x2(u.y, ptx::absmax_bf16x2(u.z, u.w)));
+        }
+      const uint32_t code = scale_code(max((big << 16) & 0x7fff0000u, big & 0x7fff0000u));
+      const float inv = code == kScaleNan ? 0.f : inverse_scale(code);
+      c.qf = scale_value(code) * f;
+#pragma unroll 1
+      for (int h = 0; h < S::kHalves; ++h)
+#pragma unroll 4
+        for (int i = 0; i < 8; ++i) {
+          uint4 *p = reinterpret_cast<uint4 *>(q + h * BM * 128 + ((i ^ (row & 7)) << 4));
+          const uint4 u = *p;
+          uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            w[k] = ptx::pack_f16(__uint_as_float(w[k] << 16) * inv, __uint_as_float(w[k] & 0xffff0000u) * inv);
+          *p = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      ptx::fence_proxy_async_smem();
+      ptx::mbar_arrive(&bars->qc_full[t]);
+      return true;
+    };
+    View c{};
+    bool have = take(c);
+    while (have && ok) {
+      if (c.nt == 0) {
         // no block of this segment is seen by the tile: an empty part
-        if (!whole && mine) g.ml[slot * 256 + t * 128 + row] = make_float2(-INFINITY, 0.f);
-        gb += nb;
+        if (!c.whole && c.mine) g.ml[c.slot * 256 + t * 128 + row] = make_float2(-INFINITY, 0.f);
+        gb += c.nb;
+        have = take(c);
         continue;
       }
-      // ---- Q: bf16 as landed -> scaled fp16 in place (the row is this thread's)
-      if (!wait_warp(&bars->q_full[t], (uint32_t)(ep & 1), abort_flag, err)) {
-        ok = false;
-        break;
-      }
-      float qf;
-      {
-        uint8_t *q = sQ + t * S::kQBytes + row * 128;
-        uint32_t amax = 0;
-#pragma unroll 1
-        for (int h = 0; h < S::kHalves; ++h)
-#pragma unroll 4
-          for (int c = 0; c < 8; ++c) {
-            const uint4 u = *reinterpret_cast<const uint4 *>(q + h * BM * 128 + ((c ^ (row & 7)) << 4));
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) amax = max(max(amax, (w[i] << 16) & 0x7fff0000u), w[i] & 0x7fff0000u);
-          }
-        const uint32_t code = scale_code(amax);
-        const float inv = code == kScaleNan ? 0.f : inverse_scale(code);
-        qf = scale_value(code) * f;
-#pragma unroll 1
-        for (int h = 0; h < S::kHalves; ++h)
-#pragma unroll 2
-          for (int c = 0; c < 8; ++c) {
-            uint4 *p = reinterpret_cast<uint4 *>(q + h * BM * 128 + ((c ^ (row & 7)) << 4));
-            const uint4 u = *p;
-            uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              w[i] = code == kScaleNan ? 0u : ptx::pack_f16(__uint_as_float(w[i] << 16) * inv,
-                                                            __uint_as_float(w[i] & 0xffff0000u) * inv);
-            *p = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        ptx::fence_proxy_async_smem();
-        ptx::mbar_arrive(&bars->qc_full[t]);
-      }
+      const int nt = c.nt, b0 = c.b0, hk = c.hk, end = c.end;
+      const int32_t *pt = c.pt;
+      const float qf = c.qf;
+      int ek = 0, ev = 0;
+      bool wide_k = false, wide_v = false;
       float m = -INFINITY, l = 0.f;                   // l counts 2^kBase per unit weight
       int evr = 0;                                    // O is in units of 2^(m + evr - kBase)
       for (int j = 0; j < nt; ++j) {                  // steps
         const int blk = gb + (j >> 1), eslot = blk % kExpSlots, buf = (gt + j) & 1;
         const uint32_t tS = lane_base + (uint32_t)(t * 128 + buf * HN);
-        if (!wait_warp(&bars->e_full[eslot], (uint32_t)((blk / kExpSlots) & 1), abort_flag, err) ||
-            !wait_warp(&bars->s_full[t][buf], (uint32_t)(((gt + j) >> 1) & 1), abort_flag, err)) {
-          ok = false;
-          break;
+        if ((j & 1) == 0) {                           // a new block's scales
+          ok = wait_warp(&bars->e_full[eslot], (uint32_t)((blk / kExpSlots) & 1), abort_flag, err);
+          ek = s_exp[eslot * 2];
+          ev = s_exp[eslot * 2 + 1];
+          wide_k = ek >= kWideBit;
+          wide_v = ev >= kWideBit;
+          ek &= 255;
+          ev &= 255;
         }
+        ok = ok && wait_warp(&bars->s_full[t][buf], (uint32_t)(((gt + j) >> 1) & 1), abort_flag, err);
+        if (!ok) break;
         const int key0 = b0 * BN + j * HN;            // the step's first key
-        const int ek = s_exp[eslot * 2] & 255, ev = s_exp[eslot * 2 + 1] & 255;
-        const bool wide_k = s_exp[eslot * 2] >= kWideBit, wide_v = s_exp[eslot * 2 + 1] >= kWideBit;
         // For a wide tile (whose codes carry no scale): the scale byte of key i, -1 if it
         // is not seen or its page is outside the pool
         auto scale_byte = [&](const uint8_t *src, int i) -> int {
@@ -815,8 +842,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           // contributions of the row may pass the units of O by 2^kRescale
           const bool need = m_new > m + kRescale || my + (float)(ev - evr) > m + kRescale;
           if (__any_sync(0xffffffffu, need)) {
-            // O must be complete up to the step before
-            if (j > 0 && !wait_warp(&bars->pv_done[t], (uint32_t)((gt + j - 1) & 1), abort_flag, err)) return false;
+            // O must be complete up to the step before.  (A barrier for each S buffer: the
+            // scores of step j came behind PV(j - 2), so the PV before on this one is over and
+            // its parity is not ambiguous.)
+            if (j > 0 && !wait_warp(&bars->pv_done[t][buf ^ 1], (uint32_t)(((gt + j - 1) >> 1) & 1), abort_flag, err))
+              return false;
             ptx::tc_fence_after();
             // The new units: the larger of the old ones and the block's largest contribution
             // (a row that has seen nothing has no old ones)
@@ -929,23 +959,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_arrive(&bars->p_full[t][buf]);
       }
       if (!ok) break;
-      gb += nb;
+      gb += c.nb;
       gt += nt;
-      // the last PV, behind the one before it: a parity tells neighbouring phases apart only
-      if ((nt > 1 && !wait_warp(&bars->pv_done[t], (uint32_t)((gt - 2) & 1), abort_flag, err)) ||
-          !wait_warp(&bars->pv_done[t], (uint32_t)((gt - 1) & 1), abort_flag, err)) {
+      // the next segment's Q before this one's output: its first scores are computed meanwhile
+      View next{};
+      have = take(next);
+      if (!ok) break;
+      if (!wait_warp(&bars->pv_done[t][(gt - 1) & 1], (uint32_t)(((gt - 1) >> 1) & 1), abort_flag, err)) {
         ok = false;
         break;
       }
       ptx::tc_fence_after();
-      ++ep;
       if (end == 0) {                                 // sees no key, whatever its q holds
         l = 0.f;
         m = -INFINITY;
       }
       // O / l is in units of 2^(evr - 127); a part keeps O in them
       const float unit = ptx::ex2((float)(evr - 127));
-      const float mul = end == 0 ? 0.f : !whole ? unit : l == 0.f ? 0.f : unit / l;
+      const float mul = end == 0 ? 0.f : !c.whole ? unit : l == 0.f ? 0.f : unit / l;
       const uint64_t once = ptx::l2_evict_first_policy();
 #pragma unroll 1
       for (int cc = 0; cc < D; cc += 32) {
@@ -956,11 +987,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::tc_fence_before();
           ptx::mbar_arrive(&bars->o_free[t]);
         }
-        if (!mine) continue;
+        if (!c.mine) continue;
 #pragma unroll
         for (int i = 0; i < 32; ++i) ov[i] = end == 0 ? 0u : __float_as_uint(__uint_as_float(ov[i]) * mul);
-        if (whole) {
-          uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + at * D + cc);
+        if (c.whole) {
+          uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + c.at * D + cc);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t o2[4];
@@ -970,32 +1001,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::st_global_hint(out + i, make_uint4(o2[0], o2[1], o2[2], o2[3]), once);
           }
         } else {
-          float4 *po = g.o + (slot * (D / 4) + cc / 4) * 256 + t * 128 + row;
+          float4 *po = g.o + (c.slot * (D / 4) + cc / 4) * 256 + t * 128 + row;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             po[i * 256] = make_float4(__uint_as_float(ov[4 * i]), __uint_as_float(ov[4 * i + 1]),
                                       __uint_as_float(ov[4 * i + 2]), __uint_as_float(ov[4 * i + 3]));
         }
       }
-      if (!mine) continue;
-      if (!whole)
-        g.ml[slot * 256 + t * 128 + row] = make_float2(m, l);
-      else if (a.lse != nullptr)
-        a.lse[at] = l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l) - kBase) * kLn2;
+      if (c.mine) {
+        if (!c.whole)
+          g.ml[c.slot * 256 + t * 128 + row] = make_float2(m, l);
+        else if (a.lse != nullptr)
+          a.lse[c.at] = l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l) - kBase) * kLn2;
+      }
+      c = next;
     }
   }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   if (warp == 12) ptx::tmem_dealloc(tmem, S::kTmemCols);
+  finish();
 }
 
 // Joins the parts of an item that several runs share (see the row-group
-// kernel's): block (i, y) joins 32 of the item's 256 rows.
+// kernel's).  Block 16 i + y joins 16 of the item's 256 rows, 16 lanes a row.
 template <int D>
 __global__ void __launch_bounds__(256) combine_kernel(const Args g) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int i = blockIdx.x, ctas = gridDim.x;
+  const int i = blockIdx.x >> 4, ctas = gridDim.x >> 4;
   const PartHead h = g.heads[i];
   if (h.begin <= 0) return;
   auto same = [&](const PartHead &p) { return p.begin > 0 && p.seq == h.seq && p.hk == h.hk && p.item == h.item; };
@@ -1003,7 +1037,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const Args g) {
   const AttendArgs &a = g.a;
   const int G = a.hq / a.hkv;
   const int q0 = a.len.cu[h.seq], q_len = a.len.cu[h.seq + 1] - q0;
-  const int r = blockIdx.y * 32 + (threadIdx.x & 31), t = r >> 7, row = r & 127;
+  const int r = (blockIdx.x & 15) * 16 + (threadIdx.x & 15), t = r >> 7, row = r & 127;
   const int tok = row / G, tk = (2 * h.item + t) * g.tpt + tok;
   if (tok >= g.tpt || tk >= q_len) return;
   int end = i + 1;
@@ -1012,23 +1046,26 @@ __global__ void __launch_bounds__(256) combine_kernel(const Args g) {
   auto slot = [&](int k) { return (size_t)(k == 0 ? 2 * (i - 1) + 1 : 2 * (i + k - 1)); };
   float M = -INFINITY, l = 0.f;
   for (int k = 0; k < parts; ++k) M = fmaxf(M, g.ml[slot(k) * 256 + r].x);
-  constexpr int NC = D / 32;                 // float4 pieces per thread: 8 threads share a row
-  const int c0 = threadIdx.x >> 5;
+  constexpr int NC = D / 64;                 // float4 pieces per thread
+  const int c0 = threadIdx.x >> 4;
   float4 acc[NC];
 #pragma unroll
   for (int c = 0; c < NC; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
   for (int k = 0; k < parts; ++k) {
     const float2 ml = g.ml[slot(k) * 256 + r];
+    float4 v[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) v[c] = g.o[(slot(k) * (D / 4) + c * 16 + c0) * 256 + r];
     if (ml.y == 0.f) continue;               // saw no key: nothing there
     const float wt = ml.x == M ? 1.f : ptx::ex2((ml.x == -INFINITY ? 0.f : ml.x) - (M == -INFINITY ? 0.f : M));
     l = fmaf(wt, ml.y, l);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const float4 v = g.o[(slot(k) * (D / 4) + c * 8 + c0) * 256 + r];
-      acc[c].x = fmaf(wt, v.x, acc[c].x);
-      acc[c].y = fmaf(wt, v.y, acc[c].y);
-      acc[c].z = fmaf(wt, v.z, acc[c].z);
-      acc[c].w = fmaf(wt, v.w, acc[c].w);
+      acc[c].x = fmaf(wt, v[c].x, acc[c].x);
+      acc[c].y = fmaf(wt, v[c].y, acc[c].y);
+      acc[c].z = fmaf(wt, v[c].z, acc[c].z);
+      acc[c].w = fmaf(wt, v[c].w, acc[c].w);
     }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -1036,7 +1073,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const Args g) {
   __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + at * D;
 #pragma unroll
   for (int c = 0; c < NC; ++c)
-    *reinterpret_cast<uint2 *>(out + (c * 8 + c0) * 4) =
+    *reinterpret_cast<uint2 *>(out + (c * 16 + c0) * 4) =
         make_uint2(ptx::pack_bf16(acc[c].x * inv, acc[c].y * inv), ptx::pack_bf16(acc[c].z * inv, acc[c].w * inv));
   if (c0 == 0 && a.lse != nullptr)
     a.lse[at] = l == 0.f ? -INFINITY : ((M == -INFINITY ? 0.f : M) + log2f(l) - kBase) * kLn2;
@@ -1070,19 +1107,9 @@ cudaError_t launch_t(const AttendArgs &a, int q_limit, int total_q, int grid, ui
   auto kern = chunk_kernel<D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
-  kern<<<grid, kThreads, S::kSmem, stream>>>(tq, tk, tv, g);
-  e = cudaGetLastError();
+  e = launch_behind(kern, grid, kThreads, S::kSmem, stream, tq, tk, tv, g);
   if (e != cudaSuccess || grid == 1) return e;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  cfg.gridDim = dim3((unsigned)grid, 8, 1);
-  cfg.blockDim = dim3(256, 1, 1);
-  cfg.stream = stream;
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, combine_kernel<D>, g);
+  return launch_behind(combine_kernel<D>, 16 * grid, 256, 0, stream, g);
 }
 
 }  // namespace

@@ -25,6 +25,24 @@ struct AttendArgs {
 __device__ __forceinline__ void store(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
+// A launch that may begin while the kernel queued before it on `stream` ends
+// (programmatic dependent launch).  Every kernel of these files waits for what it
+// reads, and at the latest before it ends, with griddepcontrol.wait.
+template <typename K, typename... Args>
+cudaError_t launch_behind(K kern, int grid, int threads, int smem, cudaStream_t stream, const Args &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Few query rows per KV head.  Sequences with q_len > q_limit are left out.
 int rows_per_group(const rpa_dims &d, int32_t max_q);
 int rows_grid(const rpa_dims &d, int32_t max_seqs, int32_t max_q, int R);
@@ -43,6 +61,7 @@ struct ChunkLayout {
   int64_t heads, ml, o, total;
 };
 ChunkLayout chunk_layout(int grid, int D);
+// It is queued with launch_behind, right behind the row-group kernels of the call.
 cudaError_t launch_chunk(const AttendArgs &a, const rpa_dims &d, int32_t max_seqs, int32_t max_q, int32_t q_limit,
                          uint8_t *ws, cudaStream_t stream);
 

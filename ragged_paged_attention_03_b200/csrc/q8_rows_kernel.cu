@@ -806,17 +806,21 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
   if (warp == 5) ptx::tmem_dealloc(tmem, S::kTmem);
 }
 
-// Joins the partial results of one group and row.  Block (i, r): the group
-// that the run at place i begins inside, if it is the first to do so; its parts
-// are slot 2 (i - 1) + 1, where the run before began the group, then 2 j of i and
-// every following place whose run begins inside the same group.
+// Joins the partial results of one group.  Block i: the group that the run at
+// place i begins inside, if it is the first to do so; its parts are slot
+// 2 (i - 1) + 1, where the run before began the group, then 2 j of i and every
+// following place whose run begins inside the same group.  D / 4 lanes take a row; where
+// there are more lanes than rows, several share a row's parts.
+constexpr int kJoinThreads = 1024;
 template <typename T, int D, int R>
-__global__ void __launch_bounds__(256) combine_kernel(const Args g) {
-  constexpr int L = D / 4, W = 256 / L;      // lanes along a row, parts in flight
+__global__ void __launch_bounds__(kJoinThreads) combine_kernel(const Args g) {
+  constexpr int L = D / 4, W = kJoinThreads / L, SL = W / R;   // lanes of a row, rows at once, shares of a row
+  static_assert(SL >= 1 && SL * R == W, "rows of a group");
   __shared__ float s_o[W][D];
   __shared__ float s_l[W];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int i = blockIdx.x, r = blockIdx.y, ctas = gridDim.x, tid = threadIdx.x;
+  const int i = blockIdx.x, places = gridDim.x, tid = threadIdx.x;
   const PartHead h = g.heads[i];
   if (h.begin <= 0) return;
   auto same = [&](const PartHead &p) { return p.begin > 0 && p.seq == h.seq && p.hk == h.hk && p.grp == h.grp; };
@@ -824,24 +828,22 @@ __global__ void __launch_bounds__(256) combine_kernel(const Args g) {
   const AttendArgs &a = g.a;
   const int G = a.hq / a.hkv;
   const int q0 = a.len.cu[h.seq], q_len = a.len.cu[h.seq + 1] - q0;
-  const int rho = h.grp * R + r;
-  if (rho >= q_len * G) return;
   int end = i + 1;
-  while (end < ctas && same(g.heads[end])) ++end;
+  while (end < places && same(g.heads[end])) ++end;
   const int parts = end - i + 1;
+  const int li = tid % L, wi = tid / L, r = wi % R, sl = wi / R;
   auto slot = [&](int k) { return ((size_t)(k == 0 ? 2 * (i - 1) + 1 : 2 * (i + k - 1))) * R + r; };
-  // the maximum of all parts, by every thread
+  // the maximum of the row's parts, by every lane
   float M = -INFINITY;
-  for (int k = tid & 31; k < parts; k += 32) M = fmaxf(M, g.ml[slot(k) * 2]);
-  M = warp_max(M);
-  const int li = tid % L, wi = tid / L;
+  for (int k = 0; k < parts; ++k) M = fmaxf(M, g.ml[slot(k) * 2]);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float l = 0.f;
-  for (int k = wi; k < parts; k += W) {
+#pragma unroll 2
+  for (int k = sl; k < parts; k += SL) {
     const float mk = g.ml[slot(k) * 2], lk = g.ml[slot(k) * 2 + 1];
+    const float4 v = *reinterpret_cast<const float4 *>(g.o + slot(k) * D + li * 4);
     if (lk == 0.f) continue;               // saw no key: nothing there
     const float wt = mk == M ? 1.f : ptx::ex2(joined(mk) - joined(M));
-    const float4 v = *reinterpret_cast<const float4 *>(g.o + slot(k) * D + li * 4);
     acc.x = fmaf(wt, v.x, acc.x);
     acc.y = fmaf(wt, v.y, acc.y);
     acc.z = fmaf(wt, v.z, acc.z);
@@ -851,16 +853,23 @@ __global__ void __launch_bounds__(256) combine_kernel(const Args g) {
   *reinterpret_cast<float4 *>(&s_o[wi][li * 4]) = acc;
   if (li == 0) s_l[wi] = l;
   __syncthreads();
-  if (tid < D) {
+  for (int e = tid; e < R * D; e += kJoinThreads) {
+    const int row = e / D, d = e % D, rho = h.grp * R + row;
+    if (rho >= q_len * G) continue;
     float v = 0.f, sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-      v += s_o[w][tid];
-      sum += s_l[w];
+    for (int w = 0; w < SL; ++w) {
+      v += s_o[w * R + row][d];
+      sum += s_l[w * R + row];
     }
-    const size_t row = (size_t)(q0 + rho / G) * a.hq + h.hk * G + rho % G;
-    store(static_cast<T *>(a.out) + row * D + tid, sum == 0.f ? 0.f : v / sum);
-    if (tid == 0 && a.lse != nullptr) a.lse[row] = sum == 0.f ? -INFINITY : (joined(M) + log2f(sum)) * kLn2;
+    const size_t at = (size_t)(q0 + rho / G) * a.hq + h.hk * G + rho % G;
+    store(static_cast<T *>(a.out) + at * D + d, sum == 0.f ? 0.f : v / sum);
+    if (d == 0 && a.lse != nullptr) {
+      float mm = -INFINITY;
+      for (int k = 0; k < parts; ++k)
+        mm = fmaxf(mm, g.ml[(((size_t)(k == 0 ? 2 * (i - 1) + 1 : 2 * (i + k - 1))) * R + row) * 2]);
+      a.lse[at] = sum == 0.f ? -INFINITY : (joined(mm) + log2f(sum)) * kLn2;
+    }
   }
 }
 
@@ -886,16 +895,7 @@ cudaError_t launch_t(const AttendArgs &a, int q_limit, int grid, uint8_t *ws, cu
   kern<<<grid, kThreads, S::kSmem, stream>>>(tk, tv, g);
   e = cudaGetLastError();
   if (e != cudaSuccess || grid == a.hkv) return e;   // one run per head: nothing is split
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  cfg.gridDim = dim3((unsigned)grid, R, 1);
-  cfg.blockDim = dim3(256, 1, 1);
-  cfg.stream = stream;
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, combine_kernel<T, D, R>, g);
+  return launch_behind(combine_kernel<T, D, R>, grid, kJoinThreads, 0, stream, g);
 }
 
 template <typename T, int D, int R> constexpr int ctas_of() { return Shape<T, D, R>::CTAS; }
