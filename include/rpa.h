@@ -530,7 +530,7 @@ RPA_API int rpa_q8_workspace_size(const rpa_dims *dims, int32_t max_seqs,
  *   rpa_q8_workspace_size bytes, else RPA_ERR_WORKSPACE.  Its contents need no
  *   initialisation and mean nothing after the call; calls that share one must
  *   be ordered on the device (two graphs that may run at once need two).
- * out and lse must not overlap any input.
+ * out must be 32-byte aligned.  out and lse must not overlap any input.
  */
 RPA_API int rpa_q8_attend(const void *q, const rpa_q8_cache *cache,
                           const int32_t *page_table, const int32_t *cu_q_lens,

@@ -767,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       c.qf = scale_value(code) * f;
 #pragma unroll 1
       for (int h = 0; h < S::kHalves; ++h)
-#pragma unroll 4
+#pragma unroll
         for (int i = 0; i < 8; ++i) {
           uint4 *p = reinterpret_cast<uint4 *>(q + h * BM * 128 + ((i ^ (row & 7)) << 4));
           const uint4 u = *p;
@@ -977,6 +977,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // O / l is in units of 2^(evr - 127); a part keeps O in them
       const float unit = ptx::ex2((float)(evr - 127));
       const float mul = end == 0 ? 0.f : !c.whole ? unit : l == 0.f ? 0.f : unit / l;
+      const uint64_t mul2 = ptx::f2_pack(mul, mul);
+      const bool blank = __any_sync(0xffffffffu, end == 0);   // a row of the warp sees no key: its O is dropped
       const uint64_t once = ptx::l2_evict_first_policy();
 #pragma unroll 1
       for (int cc = 0; cc < D; cc += 32) {
@@ -987,25 +989,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::tc_fence_before();
           ptx::mbar_arrive(&bars->o_free[t]);
         }
+        float o[32];
+#pragma unroll
+        for (int i = 0; i < 32; i += 2)
+          ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(__uint_as_float(ov[i]), __uint_as_float(ov[i + 1])), mul2), o[i], o[i + 1]);
+        if (blank) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = end == 0 ? 0.f : o[i];
+        }
         if (!c.mine) continue;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) ov[i] = end == 0 ? 0u : __float_as_uint(__uint_as_float(ov[i]) * mul);
         if (c.whole) {
-          uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + c.at * D + cc);
+          // whole 32-byte sectors: a row is this thread's, its neighbours' are far away
+          uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.out) + c.at * D + cc);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t o2[4];
+          for (int i = 0; i < 2; ++i) {
+            uint32_t o2[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              o2[k] = ptx::pack_bf16(__uint_as_float(ov[8 * i + 2 * k]), __uint_as_float(ov[8 * i + 2 * k + 1]));
-            ptx::st_global_hint(out + i, make_uint4(o2[0], o2[1], o2[2], o2[3]), once);
+            for (int k = 0; k < 8; ++k) o2[k] = ptx::pack_bf16(o[16 * i + 2 * k], o[16 * i + 2 * k + 1]);
+            ptx::st_global_hint8(out + 8 * i, o2, once);
           }
         } else {
           float4 *po = g.o + (c.slot * (D / 4) + cc / 4) * 256 + t * 128 + row;
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            po[i * 256] = make_float4(__uint_as_float(ov[4 * i]), __uint_as_float(ov[4 * i + 1]),
-                                      __uint_as_float(ov[4 * i + 2]), __uint_as_float(ov[4 * i + 3]));
+          for (int i = 0; i < 8; ++i) po[i * 256] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
       }
       if (c.mine) {

@@ -82,6 +82,7 @@ def test_misaligned(rb):
         assert io(rb, name, cache=(FAKE, FAKE + 4, FAKE, FAKE)) == 1
     assert attend(rb, q=FAKE + 2) == 1
     assert attend(rb, out=FAKE + 8) == 1
+    assert attend(rb, out=FAKE + 16) == 1
     assert attend(rb, cache=(FAKE + 1, FAKE, FAKE, FAKE)) == 1
     assert attend(rb, ws=FAKE + 128) == 8
 
