@@ -494,55 +494,65 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
     while (run.next()) {
       if (run.last_block() == run.b0) continue;
       const int qb = seg & 1;
-      if (seg >= 2 && !wait_warp(&bars->q_empty[qb], (uint32_t)(((seg >> 1) & 1) ^ 1), abort_flag, a.err)) break;
-#pragma unroll 2
-      for (int r = 0; r < R; ++r) {
-        const int rho = run.grp * R + r;
-        const bool ok = rho < run.q_len * G;
-        float x[E];
-        uint32_t amax = 0;
-        const T *src = static_cast<const T *>(a.q) +
-                       ((size_t)(run.q0 + (ok ? rho / G : 0)) * a.hq + run.hk * G + (ok ? rho % G : 0)) * D + lane * E;
-        if constexpr (sizeof(T) == 4) {
+      // every row's values first, so that their loads are one latency
+      constexpr int NW = E * (int)sizeof(T) / 4;      // words per lane and row
+      uint32_t raw[R][NW];
 #pragma unroll
-          for (int e = 0; e < E; e += 2) {
-            const float2 v = *reinterpret_cast<const float2 *>(src + e);
-            x[e] = v.x;
-            x[e + 1] = v.y;
-          }
+      for (int r = 0; r < R; ++r) {
+        const int rho = run.grp * R + r, i = rho / G;
+        const bool ok = rho < run.q_len * G;
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(
+            static_cast<const T *>(a.q) + ((size_t)(run.q0 + i) * a.hq + run.hk * G + (rho - i * G)) * D + lane * E);
+        if constexpr (NW == 1) {
+          raw[r][0] = ok ? src[0] : 0u;
+        } else if constexpr (NW == 2) {
+          const uint2 v = ok ? *reinterpret_cast<const uint2 *>(src) : make_uint2(0, 0);
+          raw[r][0] = v.x; raw[r][1] = v.y;
         } else {
 #pragma unroll
-          for (int e = 0; e < E; e += 2) {
-            const uint32_t v = *reinterpret_cast<const uint32_t *>(src + e);
-            x[e] = __uint_as_float(v << 16);
-            x[e + 1] = __uint_as_float(v & 0xffff0000u);
+          for (int w = 0; w < NW; w += 4) {
+            const uint4 v = ok ? *reinterpret_cast<const uint4 *>(src + w) : make_uint4(0, 0, 0, 0);
+            raw[r][w] = v.x; raw[r][w + 1] = v.y; raw[r][w + 2] = v.z; raw[r][w + 3] = v.w;
           }
         }
+      }
+      if (seg >= 2 && !wait_warp(&bars->q_empty[qb], (uint32_t)(((seg >> 1) & 1) ^ 1), abort_flag, a.err)) break;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float x[E];
+        uint32_t amax = 0;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          if (!ok) x[e] = 0.f;
+          if constexpr (sizeof(T) == 4) x[e] = __uint_as_float(raw[r][e]);
+          else x[e] = __uint_as_float(e & 1 ? raw[r][e / 2] & 0xffff0000u : raw[r][e / 2] << 16);
           amax = max(amax, __float_as_uint(x[e]) & 0x7fffffffu);
         }
         amax = __reduce_max_sync(0xffffffffu, amax);
         const uint32_t code = scale_code(amax);
         const float inv = code == kScaleNan ? 0.f : inverse_scale(code);
-        // byte of part p, value d: row p * R + r of the K-major tile, 16-byte chunks swizzled
 #pragma unroll
         for (int e = 0; e < E; ++e) x[e] = code == kScaleNan ? 0.f : x[e] * inv;
+        // part p of the row: row p * R + r of the K-major tile, 16-byte chunks swizzled
         const int d0 = lane * E, c = d0 / S::W, dd = d0 % S::W;
 #pragma unroll
         for (int p = 0; p < S::NQ; ++p) {
           const int row = p * R + r;
           const int sz = S::W == 128 ? row & 7 : (row >> 1) & 3;
           uint8_t *dst = sQ + qb * S::kQBuf + c * S::NQpad * S::W + row * S::W + (((dd >> 4) ^ sz) << 4) + (dd & 15);
+          uint32_t word[(E + 3) / 4] = {};
 #pragma unroll
           for (int e = 0; e < E; e += 2) {
             const uint32_t v = to_e4m3x2(x[e], x[e + 1]);
-            const float2 b = __half22float2(from_e4m3x2(v));
-            x[e] = (x[e] - b.x) * 16.f;
-            x[e + 1] = (x[e + 1] - b.y) * 16.f;
-            *reinterpret_cast<uint16_t *>(dst + e) = (uint16_t)v;
+            word[e / 4] |= v << (8 * (e & 2));
+            if (p + 1 < S::NQ) {
+              const float2 b = __half22float2(from_e4m3x2(v));
+              x[e] = (x[e] - b.x) * 16.f;
+              x[e + 1] = (x[e + 1] - b.y) * 16.f;
+            }
           }
+          if constexpr (E == 2) *reinterpret_cast<uint16_t *>(dst) = (uint16_t)word[0];
+          else if constexpr (E == 4) *reinterpret_cast<uint32_t *>(dst) = word[0];
+          else *reinterpret_cast<uint2 *>(dst) = make_uint2(word[0], word[E / 4 - 1]);
         }
         if (lane == 0) {
           s_qf[qb * 16 + r] = scale_value(code) * f;
