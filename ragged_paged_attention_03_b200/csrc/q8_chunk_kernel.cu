@@ -106,7 +106,7 @@ struct Seg {
 };
 constexpr int kSegUsers = 2 + 1 + 4 + 8;   // warps that release a slot: MMA, TMA of codes, converters, softmax
 
-static_assert(1024 + sizeof(Bars) + 20 * 8 + 2 * kExpSlots * 4 + kSegSlots * sizeof(Seg) + 8 <= 2048, "control block");
+static_assert(1024 + sizeof(Bars) + 2 * kExpSlots * 4 + kSegSlots * sizeof(Seg) + 8 <= 2048, "control block");
 
 struct PartHead {
   int32_t seq, hk, item, begin;
@@ -269,8 +269,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *sC = sV + NSV * S::kKVBytes;
   uint16_t *s_fac = reinterpret_cast<uint16_t *>(base + S::kData);   // [2][K, V][128] factors of a block's keys
   Bars *bars = reinterpret_cast<Bars *>(s_fac + 2 * 2 * BN);
-  int64_t *s_scan = reinterpret_cast<int64_t *>(bars + 1);       // [16 + 4]
-  int *s_exp = reinterpret_cast<int *>(s_scan + 20);             // [kExpSlots][2]
+  int64_t *s_scan = reinterpret_cast<int64_t *>(s_fac);          // [2 * 16 + 2], before the factors
+  int *s_exp = reinterpret_cast<int *>(bars + 1);             // [kExpSlots][2]
   Seg *s_seg = reinterpret_cast<Seg *>(s_exp + 2 * kExpSlots);   // [kSegSlots]
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_seg + kSegSlots);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -286,74 +286,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   // but what the stream holds next counts on them: every CTA waits for them as it ends.
   auto finish = [] { asm volatile("griddepcontrol.wait;" ::: "memory"); };
   // ---- this CTA's run of blocks
-  const int n = checked_seqs(a.len);
-  if (n < 0) {
-    if (cta == 0 && tid == 0) raise(err, RPA_DEV_BAD_LENGTHS);
+  const Start start = find_start<kThreads>(a.len, cta, ctas, s_scan, [&](int q_len, int kv) {
+    const SeqItems w = seq_items(q_len, kv, g);
+    return w.before(w.items) * a.hkv;
+  });
+  if (start.count == 0) {
+    if (start.n < 0 && cta == 0 && tid == 0) raise(err, RPA_DEV_BAD_LENGTHS);
     if (tid == 0) g.heads[cta].begin = 0;
     finish();
     return;
-  }
-  int64_t mine = 0;
-  for (int s = tid; s < n; s += kThreads) {
-    const SeqItems w = seq_items(a.len.cu[s + 1] - a.len.cu[s], a.len.kv[s], g);
-    mine += w.before(w.items) * a.hkv;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) s_scan[warp] = mine;
-  __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) total += s_scan[w];
-  const int64_t per = total / ctas, extra = total - per * ctas;
-  const int64_t first = per * cta + (cta < extra ? cta : extra);
-  const int64_t count = per + (cta < extra ? 1 : 0);
-  if (count == 0) {
-    if (tid == 0) g.heads[cta].begin = 0;
-    finish();
-    return;
-  }
-  int64_t before = 0;
-  for (int s0 = 0; s0 < n; s0 += kThreads) {
-    const int s = s0 + tid;
-    SeqItems w{};
-    int64_t one = 0;
-    if (s < n) {
-      w = seq_items(a.len.cu[s + 1] - a.len.cu[s], a.len.kv[s], g);
-      one = w.before(w.items);
-    }
-    const int64_t b = one * a.hkv;
-    int64_t incl = b;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    __syncthreads();
-    if (lane == 31) s_scan[warp] = incl;
-    __syncthreads();
-    int64_t excl = before + incl - b, round = 0;
-#pragma unroll
-    for (int w2 = 0; w2 < kThreads / 32; ++w2) {
-      if (w2 < warp) excl += s_scan[w2];
-      round += s_scan[w2];
-    }
-    if (first >= excl && first < excl + b) {
-      const int64_t off = first - excl;
-      const int hk = (int)(off / one);
-      const int64_t r = off - hk * one;
-      int lo = 0, hi = w.items - 1;          // the item: the largest with before(item) <= r
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (w.before(mid) <= r) lo = mid; else hi = mid - 1;
-      }
-      s_scan[16] = s;
-      s_scan[17] = hk;
-      s_scan[18] = lo;
-      s_scan[19] = r - w.before(lo);
-    }
-    before += round;
-    if (first < before) break;               // uniform
   }
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -423,13 +364,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       // --------------------------------------------- the run, TMA of Q
       Run run;
       run.g = &g;
-      run.n = n;
-      run.s = (int)s_scan[16];
-      run.hk = (int)s_scan[17];
-      run.item = (int)s_scan[18];
-      run.blk = (int)s_scan[19];
-      run.left = count;
+      run.n = start.n;
+      run.s = start.s;
+      run.left = start.count;
       run.load();
+      {
+        // the KV head, the item (the largest with before(item) <= off) and the block in it:
+        // by halves while that saves steps, then item by item
+        const int64_t one = run.w.before(run.w.items);
+        run.hk = (int)(start.off / one);
+        const int64_t off = start.off - run.hk * one;
+        int lo = 0, hi = run.w.items - 1;
+        while (hi - lo > 32) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (run.w.before(mid) <= off) lo = mid; else hi = mid - 1;
+        }
+        int64_t at = lo > 0 ? run.w.before(lo) : 0;
+        for (int nb; lo < hi && at + (nb = run.w.blocks_of(lo)) <= off; ++lo) at += nb;
+        run.item = lo;
+        run.blk = (int)(off - at);
+      }
       const uint64_t once = ptx::l2_evict_first_policy();
       int uses0 = 0, uses1 = 0;
       const uint32_t bytes = (uint32_t)(S::kHalves * 128 * g.tpt * G);

@@ -62,6 +62,100 @@ __device__ __forceinline__ int checked_seqs(const Lengths &a) {
   return __syncthreads_or(bad) ? -1 : n;
 }
 
+// A CTA's run in a list of blocks of work, the sequences' blocks in order: runs are
+// equal, the first total % ctas of them one block longer.
+struct Start {
+  int n;           // sequences; < 0: the lengths break a rule
+  int s;           // the sequence of the run's first block,
+  int64_t off;     // that block's place within it,
+  int64_t count;   // the run's blocks (0: none; s and off are not set)
+};
+
+// Checks the lengths, as checked_seqs does, and finds the CTA's run; blocks(q_len, kv_len)
+// is a sequence's number of blocks.  By all NT threads, uniform in the block; scan: shared
+// memory for 2 * NT / 32 + 2 words.  Up to NT sequences take one pass: their lengths are
+// read beside the count (entries past it lie within the arrays and are dropped).
+template <int NT, class F>
+__device__ __forceinline__ Start find_start(const Lengths &a, int cta, int ctas, int64_t *scan, F blocks) {
+  constexpr int NW = NT / 32;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int c0 = 0, c1 = 0, kv = 0;
+  if (tid < a.max_seqs) {
+    c0 = a.cu[tid];
+    c1 = a.cu[tid + 1];
+    kv = a.kv[tid];
+  }
+  const int n = *a.num_seqs;
+  int bad = n < 0 || n > a.max_seqs;
+  auto check = [&](int s, int x0, int x1, int k) {
+    const int64_t ql = (int64_t)x1 - x0;
+    bad |= ql < 0 || k < 0 || k > a.cap || (a.max_q >= 0 && ql > a.max_q) || (a.self && k < ql) ||
+           (s == 0 && x0 != 0) || (s == n - 1 && x1 > a.T);
+  };
+  auto warp_scan = [&](int64_t v) -> int64_t {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    return v;
+  };
+  int64_t b = 0, rest = 0;
+  if (!bad && tid < n) {
+    check(tid, c0, c1, kv);
+    if (!bad) b = blocks(c1 - c0, kv);
+  }
+  if (n > NT)
+    for (int s = tid + NT; !bad && s < n; s += NT) {
+      const int x0 = a.cu[s], x1 = a.cu[s + 1], k = a.kv[s];
+      check(s, x0, x1, k);
+      if (!bad) rest += blocks(x1 - x0, k);
+    }
+  int64_t incl = warp_scan(b);
+  if (lane == 31) scan[warp] = incl;
+  rest = n > NT ? warp_scan(rest) : 0;
+  if (lane == 31) scan[NW + warp] = rest;
+  if (__syncthreads_or(bad)) return Start{-1, 0, 0, 0};
+  int64_t excl = incl - b, tile = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    if (w < warp) excl += scan[w];
+    tile += scan[w];
+    total += scan[w] + scan[NW + w];
+  }
+  const int64_t per = total / ctas, extra = total - per * ctas;
+  const int64_t first = per * cta + (cta < extra ? cta : extra);
+  Start r{n, 0, 0, per + (cta < extra ? 1 : 0)};
+  if (r.count == 0) return r;
+  if (first >= excl && first < excl + b) {
+    scan[2 * NW] = tid;
+    scan[2 * NW + 1] = first - excl;
+  }
+  int64_t before = tile;
+  for (int s0 = NT; first >= before; s0 += NT) {   // uniform; only with more than NT sequences
+    const int s = s0 + tid;
+    b = s < n ? blocks(a.cu[s + 1] - a.cu[s], a.kv[s]) : 0;
+    incl = warp_scan(b);
+    __syncthreads();                               // the sums of the round before have been read
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    excl = before + incl - b;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      if (w < warp) excl += scan[w];
+      before += scan[w];
+    }
+    if (first >= excl && first < excl + b) {
+      scan[2 * NW] = s;
+      scan[2 * NW + 1] = first - excl;
+    }
+  }
+  __syncthreads();
+  r.s = (int)scan[2 * NW];
+  r.off = scan[2 * NW + 1];
+  return r;
+}
+
 // The sequence that holds token t: the largest s in [0, n) with cu[s] <= t.
 __device__ __forceinline__ int seq_of(const int32_t *cu, int n, int t) {
   int lo = 0, hi = n - 1;

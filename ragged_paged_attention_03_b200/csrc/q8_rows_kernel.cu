@@ -42,6 +42,7 @@
 // (cp.async).  Everything runs ahead across groups through rings in shared
 // memory.
 #include <cuda.h>
+#include <limits.h>
 #include <math.h>
 
 #include <algorithm>
@@ -80,7 +81,7 @@ struct Shape {
   static constexpr int kTile = BN * D;                           // K or V codes of a block
   static constexpr int kQBuf = NQpad * D;
   static constexpr int kPBuf = NPpad * BN;
-  static constexpr int kFixed = 1024 + 2 * kQBuf + 2 * kPBuf + kScaleSlots * 2 * BN + 2560;
+  static constexpr int kFixed = 1024 + 2 * kQBuf + 2 * kPBuf + kScaleSlots * 2 * BN + 2816;
   static constexpr int kTmem = pow2_cols(2 * NQpad + 2 * NPpad * CT);
   // CTAs per SM: three where their TMEM, registers and two-slot rings fit
   static constexpr int kSmMax = 227 * 1024;
@@ -183,12 +184,6 @@ struct Run {
     blk = 0;
     return true;
   }
-  // keys seen by row `row` of the group, and by its last row
-  __device__ __forceinline__ int row_end(int row) const {
-    const int rho = grp * R + row;
-    if (rho >= q_len * G) return 0;
-    return a->causal ? min(kv, max(0, kv - q_len + rho / G + 1)) : kv;
-  }
   // the segment's last block that any row sees, plus one (>= b0)
   __device__ __forceinline__ int last_block() const {
     const int rho = min((grp + 1) * R, q_len * G) - 1;
@@ -241,10 +236,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
   Bars *bars = reinterpret_cast<Bars *>(sSc + kScaleSlots * 2 * BN);
   float *s_qf = reinterpret_cast<float *>(bars + 1);       // [2][16] row factors
   int *s_end = reinterpret_cast<int *>(s_qf + 32);         // [2][16] keys each row sees
-  float *s_max = reinterpret_cast<float *>(s_end + 32);    // [2][4][16 + 16] warps' maxima of x, x + ev
+  long long *s_at = reinterpret_cast<long long *>(s_end + 32);   // [2][16] the rows' places in out, -1: none
+  float *s_max = reinterpret_cast<float *>(s_at + 32);    // [2][4][16 + 16] warps' maxima of x, x + ev
   float *s_l = reinterpret_cast<float *>(s_max + 256);       // [4][16]
-  int64_t *s_scan = reinterpret_cast<int64_t *>(s_l + 64); // [8 + 3]
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_scan + 12);
+  float *s_ml = s_l + 64;                                  // [16][2] maximum and sum of a finished group
+  int64_t *s_scan = reinterpret_cast<int64_t *>(s_ml + 32); // [2 * 8 + 2]
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_scan + 18);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
   const AttendArgs &a = g.a;
@@ -255,61 +252,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
   const int G = a.hq / a.hkv;
 
   // ---- this CTA's run of blocks
-  const int n = checked_seqs(a.len);
-  if (n < 0) {
-    if (blockIdx.x == 0 && tid == 0) raise(a.err, RPA_DEV_BAD_LENGTHS);
+  const Start start = find_start<kThreads>(a.len, cta, ctas, s_scan, [&](int q_len, int kv) {
+    return seq_work<R>(q_len, kv, G, g.q_limit).blocks();
+  });
+  if (start.count == 0) {
+    if (start.n < 0 && blockIdx.x == 0 && tid == 0) raise(a.err, RPA_DEV_BAD_LENGTHS);
     if (tid == 0) g.heads[place].begin = 0;
     return;
-  }
-  int64_t mine = 0;
-  for (int s = tid; s < n; s += kThreads)
-    mine += seq_work<R>(a.len.cu[s + 1] - a.len.cu[s], a.len.kv[s], G, g.q_limit).blocks();
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) s_scan[warp] = mine;
-  __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) total += s_scan[w];
-  // equal runs: the first `total % ctas` CTAs take one block more
-  const int64_t per = total / ctas, extra = total - per * ctas;
-  const int64_t first = per * cta + (cta < extra ? cta : extra);
-  const int64_t count = per + (cta < extra ? 1 : 0);
-  if (count == 0) {
-    if (tid == 0) g.heads[place].begin = 0;
-    return;
-  }
-  // the sequence holding block `first`: a scan over the sequences, 256 at a time
-  int64_t before = 0;
-  for (int s0 = 0; s0 < n; s0 += kThreads) {
-    const int s = s0 + tid;
-    SeqWork w{0, 1};
-    if (s < n) w = seq_work<R>(a.len.cu[s + 1] - a.len.cu[s], a.len.kv[s], G, g.q_limit);
-    const int64_t b = w.blocks();
-    int64_t incl = b;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    __syncthreads();                    // s_scan of the previous round has been read
-    if (lane == 31) s_scan[warp] = incl;
-    __syncthreads();
-    int64_t excl = before + incl - b;
-    int64_t round = 0;
-#pragma unroll
-    for (int w2 = 0; w2 < kThreads / 32; ++w2) {
-      if (w2 < warp) excl += s_scan[w2];
-      round += s_scan[w2];
-    }
-    if (first >= excl && first < excl + b) {
-      const int64_t off = first - excl;
-      s_scan[8] = s;
-      s_scan[9] = off / w.nb;
-      s_scan[10] = off % w.nb;
-    }
-    before += round;
-    if (first < before) break;          // uniform
   }
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
@@ -356,14 +305,17 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
 
   Run<R> run;
   run.a = &a;
-  run.n = n;
+  run.n = start.n;
   run.G = G;
   run.q_limit = g.q_limit;
-  run.s = (int)s_scan[8];
   run.hk = hk;
-  run.grp_next = (int)s_scan[9];
-  run.blk = (int)s_scan[10];
-  run.left = count;
+  run.s = start.s;
+  {
+    const int nb = seq_work<R>(1, a.len.kv[start.s], G, INT_MAX).nb;
+    run.grp_next = (int)(start.off / nb);
+    run.blk = (int)(start.off - (int64_t)run.grp_next * nb);
+  }
+  run.left = start.count;
 
   if (warp == 4) {
     // ------------------------------------------------------------ TMA
@@ -491,40 +443,66 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
     int seg = 0;
     constexpr int E = D / 32;          // values per lane
     const float f = a.scale * kLog2e;
+    // Short rolled loops: a segment's code is cold, and fetching it unrolled took several
+    // times the work.  The rows land (cp.async, all in flight at once) in the very slots
+    // that their parts will take: a value has at least as many parts as bytes.
+    const int d0 = lane * E, c = d0 / S::W, dd = d0 % S::W;
+    constexpr int NB = E * (int)sizeof(T);             // bytes of a row per lane
+    auto slot_of = [&](int qb, int p, int r) -> uint8_t * {   // lane's values of part p, row r
+      const int row = p * R + r, sz = S::W == 128 ? row & 7 : (row >> 1) & 3;
+      return sQ + qb * S::kQBuf + c * S::NQpad * S::W + row * S::W + (((dd >> 4) ^ sz) << 4) + (dd & 15);
+    };
     while (run.next()) {
       if (run.last_block() == run.b0) continue;
       const int qb = seg & 1;
-      // every row's values first, so that their loads are one latency
-      constexpr int NW = E * (int)sizeof(T) / 4;      // words per lane and row
-      uint32_t raw[R][NW];
-#pragma unroll
+      if (seg >= 2 && !wait_warp(&bars->q_empty[qb], (uint32_t)(((seg >> 1) & 1) ^ 1), abort_flag, a.err)) break;
+      // row r of the group: token and head, advanced by one head a row
+      int i = run.grp * R / G, h = run.grp * R - i * G;
+#pragma unroll 1
       for (int r = 0; r < R; ++r) {
-        const int rho = run.grp * R + r, i = rho / G;
-        const bool ok = rho < run.q_len * G;
-        const uint32_t *src = reinterpret_cast<const uint32_t *>(
-            static_cast<const T *>(a.q) + ((size_t)(run.q0 + i) * a.hq + run.hk * G + (rho - i * G)) * D + lane * E);
-        if constexpr (NW == 1) {
-          raw[r][0] = ok ? src[0] : 0u;
-        } else if constexpr (NW == 2) {
-          const uint2 v = ok ? *reinterpret_cast<const uint2 *>(src) : make_uint2(0, 0);
-          raw[r][0] = v.x; raw[r][1] = v.y;
-        } else {
+        const bool ok = i < run.q_len;
+        const size_t at = (size_t)(run.q0 + i) * a.hq + hk * G + h;
+        const uint8_t *src = reinterpret_cast<const uint8_t *>(static_cast<const T *>(a.q) + at * D) + lane * NB;
 #pragma unroll
-          for (int w = 0; w < NW; w += 4) {
-            const uint4 v = ok ? *reinterpret_cast<const uint4 *>(src + w) : make_uint4(0, 0, 0, 0);
-            raw[r][w] = v.x; raw[r][w + 1] = v.y; raw[r][w + 2] = v.z; raw[r][w + 3] = v.w;
+        for (int b = 0; b < (int)sizeof(T); ++b) {
+          uint8_t *dst = slot_of(qb, b, r);
+          if constexpr (E >= 4) {
+            if (ok)
+              asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(ptx::smem_u32(dst)), "l"(src + b * E), "n"(E)
+                           : "memory");
+            else if constexpr (E == 4) *reinterpret_cast<uint32_t *>(dst) = 0;
+            else *reinterpret_cast<uint2 *>(dst) = make_uint2(0, 0);
+          } else {
+            *reinterpret_cast<uint16_t *>(dst) = ok ? *reinterpret_cast<const uint16_t *>(src + b * E) : (uint16_t)0;
           }
         }
+        if (lane == 0) {
+          s_at[qb * 16 + r] = ok ? (long long)at : -1;
+          s_end[qb * 16 + r] = !ok ? 0 : a.causal ? min(run.kv, max(0, run.kv - run.q_len + i + 1)) : run.kv;
+        }
+        if (++h == G) h = 0, ++i;
       }
-      if (seg >= 2 && !wait_warp(&bars->q_empty[qb], (uint32_t)(((seg >> 1) & 1) ^ 1), abort_flag, a.err)) break;
-#pragma unroll
+      asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 1
       for (int r = 0; r < R; ++r) {
+        uint32_t raw[(NB + 3) / 4] = {};
+#pragma unroll
+        for (int b = 0; b < (int)sizeof(T); ++b) {
+          const uint8_t *src = slot_of(qb, b, r);      // bytes [b E, + E) of the lane's share
+          if constexpr (E == 2) raw[b / 2] |= (uint32_t)*reinterpret_cast<const uint16_t *>(src) << (16 * (b & 1));
+          else if constexpr (E == 4) raw[b] = *reinterpret_cast<const uint32_t *>(src);
+          else {
+            const uint2 v = *reinterpret_cast<const uint2 *>(src);
+            raw[2 * b] = v.x;
+            raw[2 * b + 1] = v.y;
+          }
+        }
         float x[E];
         uint32_t amax = 0;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          if constexpr (sizeof(T) == 4) x[e] = __uint_as_float(raw[r][e]);
-          else x[e] = __uint_as_float(e & 1 ? raw[r][e / 2] & 0xffff0000u : raw[r][e / 2] << 16);
+          if constexpr (sizeof(T) == 4) x[e] = __uint_as_float(raw[e]);
+          else x[e] = __uint_as_float(e & 1 ? raw[e / 2] & 0xffff0000u : raw[e / 2] << 16);
           amax = max(amax, __float_as_uint(x[e]) & 0x7fffffffu);
         }
         amax = __reduce_max_sync(0xffffffffu, amax);
@@ -532,13 +510,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
         const float inv = code == kScaleNan ? 0.f : inverse_scale(code);
 #pragma unroll
         for (int e = 0; e < E; ++e) x[e] = code == kScaleNan ? 0.f : x[e] * inv;
-        // part p of the row: row p * R + r of the K-major tile, 16-byte chunks swizzled
-        const int d0 = lane * E, c = d0 / S::W, dd = d0 % S::W;
 #pragma unroll
         for (int p = 0; p < S::NQ; ++p) {
-          const int row = p * R + r;
-          const int sz = S::W == 128 ? row & 7 : (row >> 1) & 3;
-          uint8_t *dst = sQ + qb * S::kQBuf + c * S::NQpad * S::W + row * S::W + (((dd >> 4) ^ sz) << 4) + (dd & 15);
           uint32_t word[(E + 3) / 4] = {};
 #pragma unroll
           for (int e = 0; e < E; e += 2) {
@@ -550,14 +523,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
               x[e + 1] = (x[e + 1] - b.y) * 16.f;
             }
           }
+          uint8_t *dst = slot_of(qb, p, r);
           if constexpr (E == 2) *reinterpret_cast<uint16_t *>(dst) = (uint16_t)word[0];
           else if constexpr (E == 4) *reinterpret_cast<uint32_t *>(dst) = word[0];
           else *reinterpret_cast<uint2 *>(dst) = make_uint2(word[0], word[E / 4 - 1]);
         }
-        if (lane == 0) {
-          s_qf[qb * 16 + r] = scale_value(code) * f;
-          s_end[qb * 16 + r] = run.row_end(r);
-        }
+        if (lane == 0) s_qf[qb * 16 + r] = scale_value(code) * f;
       }
       ptx::fence_proxy_async_smem();
       ptx::mbar_arrive(&bars->q_full[qb]);
@@ -606,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
   } else {
     // -------------------------------------- softmax, weights, output
     const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-    int gb = 0, seg = 0;
+    int gb = 0, seg = 0, qseg = 0;
     bool ok = true;
     bool head_written = false;
     while (ok && run.next()) {
@@ -758,7 +729,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
           ok = false;
           break;
         }
-        ptx::mbar_arrive(&bars->q_empty[seg & 1]);
         // row sums of the 128 keys' threads
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -771,39 +741,51 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
           ok = false;
           break;
         }
-        ++seg;
+        qseg = seg++;
         // (s_l is written again only behind the next segment's first x_full)
 #pragma unroll
         for (int r = 0; r < R; ++r) l[r] = (s_l[r] + s_l[16 + r]) + (s_l[32 + r] + s_l[48 + r]);
       }
       const bool whole = run.b0 == 0 && run.b1 == run.nb;
-      if (whole) {
+      // 2 * place: the run begins inside the group; 2 * place + 1: it begins with it
+      const size_t slot = 2 * (size_t)place + (run.b0 > 0 ? 0 : 1);
+      const long long *at = s_at + (qseg & 1) * 16;   // (whole groups have been through the Q warp)
+      if (tid == 0) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          const int rho = run.grp * R + r;
-          if (rho >= run.q_len * G) continue;
-          const size_t row = (size_t)(run.q0 + rho / G) * a.hq + run.hk * G + rho % G;
-          const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
-#pragma unroll
-          for (int c = 0; c < S::CT; ++c)
-            if (D >= 128 || tid < D) store(static_cast<T *>(a.out) + row * D + c * 128 + tid, o[c][r] * inv);
-          if (tid == 0 && a.lse != nullptr)
-            a.lse[row] = l[r] == 0.f ? -INFINITY : (joined(m[r]) + log2f(l[r])) * kLn2;
+          s_ml[2 * r] = m[r];
+          s_ml[2 * r + 1] = l[r];
         }
-      } else {
-        // 2 * place: the run begins inside the group; 2 * place + 1: it begins with it
-        const size_t slot = 2 * (size_t)place + (run.b0 > 0 ? 0 : 1);
+      }
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
+      for (int r = 0; r < R; ++r) {
+        if (whole) {
+          const long long row = at[r];
+          const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+          if (row >= 0)
+#pragma unroll
+            for (int c = 0; c < S::CT; ++c)
+              if (D >= 128 || tid < D) store(static_cast<T *>(a.out) + row * D + c * 128 + tid, o[c][r] * inv);
+        } else {
 #pragma unroll
           for (int c = 0; c < S::CT; ++c)
             if (D >= 128 || tid < D) g.o[(slot * R + r) * D + c * 128 + tid] = o[c][r];
-          if (tid == 0) {
-            g.ml[(slot * R + r) * 2] = m[r];
-            g.ml[(slot * R + r) * 2 + 1] = l[r];
-          }
         }
       }
+      if (warp == 0) {
+        __syncwarp();
+        if (lane < R) {
+          const float mr = s_ml[2 * lane], lr = s_ml[2 * lane + 1];
+          if (!whole) {
+            g.ml[(slot * R + lane) * 2] = mr;
+            g.ml[(slot * R + lane) * 2 + 1] = lr;
+          } else if (a.lse != nullptr && at[lane] >= 0) {
+            a.lse[at[lane]] = lr == 0.f ? -INFINITY : (joined(mr) + log2f(lr)) * kLn2;
+          }
+        }
+        __syncwarp();
+      }
+      if (last > run.b0) ptx::mbar_arrive(&bars->q_empty[qseg & 1]);
       if (!head_written && tid == 0)
         g.heads[place] = PartHead{run.s, hk, run.grp, run.b0};
       head_written = true;
