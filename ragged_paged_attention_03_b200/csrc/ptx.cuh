@@ -187,6 +187,12 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// 1 / x on the multi-function unit (within one unit in the last place).
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // ---------------------------------------------------------------- tcgen05
 // TMEM addresses: bits [31:16] lane, [15:0] column.

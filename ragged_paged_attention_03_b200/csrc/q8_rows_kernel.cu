@@ -37,10 +37,11 @@
 // combine_kernel, queued behind with programmatic dependent launch, joins them
 // in the order of the keys (the same bits every time).
 //
-// Warps: 0-3 softmax, weights and output (thread = key of the block, then row of
-// O^T), 4 TMA of K and V tiles, 5 MMA issue, 6 the parts of Q, 7 the scales
-// (cp.async).  Everything runs ahead across groups through rings in shared
-// memory.
+// Warps: 0-3 the parts of Q (a row each at a time; one warp for all of them took
+// 12,000 clocks for 16 rows, more than many a group's keys), softmax, weights and
+// output (thread = key of the block, then row of O^T), 4 TMA of K and V tiles,
+// 5 MMA issue, 6 the scales (cp.async).  4 and 6 run ahead across groups through
+// rings in shared memory.
 #include <cuda.h>
 #include <limits.h>
 #include <math.h>
@@ -56,7 +57,7 @@ namespace rpa {
 namespace q8 {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 224;
 constexpr int BN = 128;               // keys per block
 constexpr int kScaleSlots = 8;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -81,7 +82,7 @@ struct Shape {
   static constexpr int kTile = BN * D;                           // K or V codes of a block
   static constexpr int kQBuf = NQpad * D;
   static constexpr int kPBuf = NPpad * BN;
-  static constexpr int kFixed = 1024 + 2 * kQBuf + 2 * kPBuf + kScaleSlots * 2 * BN + 2816;
+  static constexpr int kFixed = 1024 + kQBuf + 2 * kPBuf + kScaleSlots * 2 * BN + 2816;
   static constexpr int kTmem = pow2_cols(2 * NQpad + 2 * NPpad * CT);
   // CTAs per SM: three where their TMEM, registers and two-slot rings fit
   static constexpr int kSmMax = 227 * 1024;
@@ -102,7 +103,7 @@ struct Shape {
 struct Bars {
   uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8];
   uint64_t s_full[2], p_full[2], pv_full[2];
-  uint64_t q_full[2], q_empty[2];
+  uint64_t q_full;
   uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots];
   uint64_t x_full[2], l_full;    // the softmax warps' maxima and sums are in shared memory
   uint64_t drain;
@@ -230,8 +231,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
   uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *sK = base;
   uint8_t *sV = sK + NS * S::kTile;
-  uint8_t *sQ = sV + NS * S::kTile;                        // two buffers
-  uint8_t *sP = sQ + 2 * S::kQBuf;                         // two buffers
+  uint8_t *sQ = sV + NS * S::kTile;
+  uint8_t *sP = sQ + S::kQBuf;                             // two buffers
   uint8_t *sSc = sP + 2 * S::kPBuf;                        // [slot][K, V][128]
   Bars *bars = reinterpret_cast<Bars *>(sSc + kScaleSlots * 2 * BN);
   float *s_qf = reinterpret_cast<float *>(bars + 1);       // [2][16] row factors
@@ -271,13 +272,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
       ptx::mbar_init(&bars->s_full[i], 1);
       ptx::mbar_init(&bars->p_full[i], 128);
       ptx::mbar_init(&bars->pv_full[i], 1);
-      ptx::mbar_init(&bars->q_full[i], 32);
-      ptx::mbar_init(&bars->q_empty[i], 1 + 128);   // the last QK's commit and the softmax threads
     }
     for (int i = 0; i < kScaleSlots; ++i) {
       ptx::mbar_init(&bars->sc_full[i], 32);
       ptx::mbar_init(&bars->sc_empty[i], 128);
     }
+    ptx::mbar_init(&bars->q_full, 128);
     ptx::mbar_init(&bars->x_full[0], 4);
     ptx::mbar_init(&bars->x_full[1], 4);
     ptx::mbar_init(&bars->l_full, 4);
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
   }
   // columns that no part fills are zeros
   if (S::NQpad > S::CQ)
-    for (int i = tid; i < 2 * S::kQBuf / 16; i += kThreads) reinterpret_cast<uint4 *>(sQ)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < S::kQBuf / 16; i += kThreads) reinterpret_cast<uint4 *>(sQ)[i] = make_uint4(0, 0, 0, 0);
   ptx::fence_proxy_async_smem();
   ptx::tc_fence_before();
   __syncthreads();
@@ -385,8 +385,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
     const uint64_t dp0 = ptx::umma_desc(ptx::smem_u32(sP), 128, BN * 16, 0);
     int gb = 0, seg = 0;
     bool ok = true;
-    // QK of block `blk` (ring position) of the segment in Q buffer `qb`
-    auto qk = [&](int blk, int qb) -> bool {
+    // QK of block `blk` (ring position)
+    auto qk = [&](int blk) -> bool {
       const int st = blk % NS;
       if (!wait_warp(&bars->k_full[st], (uint32_t)((blk / NS) & 1), abort_flag, a.err)) return false;
       ptx::tc_fence_after();
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
         const int c = k * 32 / S::W, kk = k * 32 % S::W;
         ptx::umma_ss_e4m3_elect(tS + (blk & 1) * S::NQpad,
                                 dk0 + (uint64_t)((st * S::kTile + c * BN * S::W + kk) >> 4),
-                                dq0 + (uint64_t)((qb * S::kQBuf + c * S::NQpad * S::W + kk) >> 4), idesc_qk, k > 0);
+                                dq0 + (uint64_t)((c * S::NQpad * S::W + kk) >> 4), idesc_qk, k > 0);
       }
       ptx::umma_commit_elect(&bars->s_full[blk & 1]);
       ptx::umma_commit_elect(&bars->k_empty[st]);
@@ -417,124 +417,25 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
       ptx::umma_commit_elect(&bars->v_empty[st]);
       return true;
     };
-    // Blocks of all segments in one chain: QK runs one block ahead of PV.  The
-    // S buffer of QK(b) was read before P(b - 2) was published, which PV(b - 2),
-    // issued earlier, waited for; the O and P buffers of PV(b) are free once
-    // P(b) is published (the softmax threads read PV(b - 2) before that).
-    int pending = -1;
+    // Within a segment QK runs one block ahead of PV.  The S buffer of QK(b) was read
+    // before P(b - 2) was published, which PV(b - 2), issued earlier, waited for; the O and
+    // P buffers of PV(b) are free once P(b) is published (the softmax threads read PV(b - 2)
+    // before that).  The next segment's Q comes when this one's last PV has been read.
     while (ok && run.next()) {
       const int last = run.last_block();
       if (last == run.b0) continue;
-      ok = wait_warp(&bars->q_full[seg & 1], (uint32_t)((seg >> 1) & 1), abort_flag, a.err);
+      ok = wait_warp(&bars->q_full, (uint32_t)(seg & 1), abort_flag, a.err);
       for (int b = run.b0; ok && b < last; ++b, ++gb) {
-        ok = qk(gb, seg & 1);
-        if (ok && b + 1 == last) ptx::umma_commit_elect(&bars->q_empty[seg & 1]);
-        if (ok && pending >= 0) ok = pv(pending);
-        pending = gb;
+        ok = qk(gb);
+        if (ok && b > run.b0) ok = pv(gb - 1);
       }
+      if (ok) ok = pv(gb - 1);
       ++seg;
     }
-    if (ok && pending >= 0) pv(pending);
     ptx::umma_commit_elect(&bars->drain);
     ptx::mbar_wait(&bars->drain, 0);
     __syncwarp();
   } else if (warp == 6) {
-    // ------------------------------------------------- the parts of Q
-    int seg = 0;
-    constexpr int E = D / 32;          // values per lane
-    const float f = a.scale * kLog2e;
-    // Short rolled loops: a segment's code is cold, and fetching it unrolled took several
-    // times the work.  The rows land (cp.async, all in flight at once) in the very slots
-    // that their parts will take: a value has at least as many parts as bytes.
-    const int d0 = lane * E, c = d0 / S::W, dd = d0 % S::W;
-    constexpr int NB = E * (int)sizeof(T);             // bytes of a row per lane
-    auto slot_of = [&](int qb, int p, int r) -> uint8_t * {   // lane's values of part p, row r
-      const int row = p * R + r, sz = S::W == 128 ? row & 7 : (row >> 1) & 3;
-      return sQ + qb * S::kQBuf + c * S::NQpad * S::W + row * S::W + (((dd >> 4) ^ sz) << 4) + (dd & 15);
-    };
-    while (run.next()) {
-      if (run.last_block() == run.b0) continue;
-      const int qb = seg & 1;
-      if (seg >= 2 && !wait_warp(&bars->q_empty[qb], (uint32_t)(((seg >> 1) & 1) ^ 1), abort_flag, a.err)) break;
-      // row r of the group: token and head, advanced by one head a row
-      int i = run.grp * R / G, h = run.grp * R - i * G;
-#pragma unroll 1
-      for (int r = 0; r < R; ++r) {
-        const bool ok = i < run.q_len;
-        const size_t at = (size_t)(run.q0 + i) * a.hq + hk * G + h;
-        const uint8_t *src = reinterpret_cast<const uint8_t *>(static_cast<const T *>(a.q) + at * D) + lane * NB;
-#pragma unroll
-        for (int b = 0; b < (int)sizeof(T); ++b) {
-          uint8_t *dst = slot_of(qb, b, r);
-          if constexpr (E >= 4) {
-            if (ok)
-              asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(ptx::smem_u32(dst)), "l"(src + b * E), "n"(E)
-                           : "memory");
-            else if constexpr (E == 4) *reinterpret_cast<uint32_t *>(dst) = 0;
-            else *reinterpret_cast<uint2 *>(dst) = make_uint2(0, 0);
-          } else {
-            *reinterpret_cast<uint16_t *>(dst) = ok ? *reinterpret_cast<const uint16_t *>(src + b * E) : (uint16_t)0;
-          }
-        }
-        if (lane == 0) {
-          s_at[qb * 16 + r] = ok ? (long long)at : -1;
-          s_end[qb * 16 + r] = !ok ? 0 : a.causal ? min(run.kv, max(0, run.kv - run.q_len + i + 1)) : run.kv;
-        }
-        if (++h == G) h = 0, ++i;
-      }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-#pragma unroll 1
-      for (int r = 0; r < R; ++r) {
-        uint32_t raw[(NB + 3) / 4] = {};
-#pragma unroll
-        for (int b = 0; b < (int)sizeof(T); ++b) {
-          const uint8_t *src = slot_of(qb, b, r);      // bytes [b E, + E) of the lane's share
-          if constexpr (E == 2) raw[b / 2] |= (uint32_t)*reinterpret_cast<const uint16_t *>(src) << (16 * (b & 1));
-          else if constexpr (E == 4) raw[b] = *reinterpret_cast<const uint32_t *>(src);
-          else {
-            const uint2 v = *reinterpret_cast<const uint2 *>(src);
-            raw[2 * b] = v.x;
-            raw[2 * b + 1] = v.y;
-          }
-        }
-        float x[E];
-        uint32_t amax = 0;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          if constexpr (sizeof(T) == 4) x[e] = __uint_as_float(raw[e]);
-          else x[e] = __uint_as_float(e & 1 ? raw[e / 2] & 0xffff0000u : raw[e / 2] << 16);
-          amax = max(amax, __float_as_uint(x[e]) & 0x7fffffffu);
-        }
-        amax = __reduce_max_sync(0xffffffffu, amax);
-        const uint32_t code = scale_code(amax);
-        const float inv = code == kScaleNan ? 0.f : inverse_scale(code);
-#pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = code == kScaleNan ? 0.f : x[e] * inv;
-#pragma unroll
-        for (int p = 0; p < S::NQ; ++p) {
-          uint32_t word[(E + 3) / 4] = {};
-#pragma unroll
-          for (int e = 0; e < E; e += 2) {
-            const uint32_t v = to_e4m3x2(x[e], x[e + 1]);
-            word[e / 4] |= v << (8 * (e & 2));
-            if (p + 1 < S::NQ) {
-              const float2 b = __half22float2(from_e4m3x2(v));
-              x[e] = (x[e] - b.x) * 16.f;
-              x[e + 1] = (x[e + 1] - b.y) * 16.f;
-            }
-          }
-          uint8_t *dst = slot_of(qb, p, r);
-          if constexpr (E == 2) *reinterpret_cast<uint16_t *>(dst) = (uint16_t)word[0];
-          else if constexpr (E == 4) *reinterpret_cast<uint32_t *>(dst) = word[0];
-          else *reinterpret_cast<uint2 *>(dst) = make_uint2(word[0], word[E / 4 - 1]);
-        }
-        if (lane == 0) s_qf[qb * 16 + r] = scale_value(code) * f;
-      }
-      ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(&bars->q_full[qb]);
-      ++seg;
-    }
-  } else if (warp == 7) {
     // ------------------------------------------------------ the scales
     int gb = 0;
     bool ok = true;
@@ -577,10 +478,88 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
   } else {
     // -------------------------------------- softmax, weights, output
     const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-    int gb = 0, seg = 0, qseg = 0;
+    int gb = 0, seg = 0;
     bool ok = true;
     bool head_written = false;
-    while (ok && run.next()) {
+    constexpr int E = D / 32, RW = R / 4;   // values per lane of a row, rows per warp
+    // The parts of the current segment's query rows, and the rows' factors, places and
+    // key counts.  (The scores of the segment before have been read, so Q is free.)
+    auto prepare = [&]() {
+      constexpr int NW = E * (int)sizeof(T) / 4;      // words per lane and row
+      uint32_t raw[RW][NW];
+      int qb = (seg & 1) * 16;
+#pragma unroll
+      for (int k = 0; k < RW; ++k) {                  // every row's loads first: one latency
+        const int r = warp + 4 * k, rho = run.grp * R + r, i = rho / G;
+        const bool row_ok = i < run.q_len;
+        const size_t at = ((size_t)(run.q0 + i) * a.hq + hk * G + (rho - i * G)) * D;
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(static_cast<const T *>(a.q) + at) + lane * NW;
+        if constexpr (NW == 1) {
+          raw[k][0] = row_ok ? src[0] : 0u;
+        } else if constexpr (NW == 2) {
+          const uint2 v = row_ok ? *reinterpret_cast<const uint2 *>(src) : make_uint2(0, 0);
+          raw[k][0] = v.x;
+          raw[k][1] = v.y;
+        } else {
+#pragma unroll
+          for (int w = 0; w < NW; w += 4) {
+            const uint4 v = row_ok ? *reinterpret_cast<const uint4 *>(src + w) : make_uint4(0, 0, 0, 0);
+            raw[k][w] = v.x;
+            raw[k][w + 1] = v.y;
+            raw[k][w + 2] = v.z;
+            raw[k][w + 3] = v.w;
+          }
+        }
+        if (lane == 0) {
+          s_at[qb + r] = row_ok ? (long long)at : -1;
+          s_end[qb + r] = !row_ok ? 0 : a.causal ? min(run.kv, max(0, run.kv - run.q_len + i + 1)) : run.kv;
+        }
+      }
+      const int d0 = lane * E, c = d0 / S::W, dd = d0 % S::W;
+#pragma unroll
+      for (int k = 0; k < RW; ++k) {
+        const int r = warp + 4 * k;
+        float x[E];
+        uint32_t amax = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          if constexpr (sizeof(T) == 4) x[e] = __uint_as_float(raw[k][e]);
+          else x[e] = __uint_as_float(e & 1 ? raw[k][e / 2] & 0xffff0000u : raw[k][e / 2] << 16);
+          amax = max(amax, __float_as_uint(x[e]) & 0x7fffffffu);
+        }
+        amax = __reduce_max_sync(0xffffffffu, amax);
+        const uint32_t code = scale_code(amax);
+        const float inv = code == kScaleNan ? 0.f : inverse_scale(code);
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = code == kScaleNan ? 0.f : x[e] * inv;
+        // part p of the row: row p * R + r of the K-major tile, 16-byte chunks swizzled
+#pragma unroll
+        for (int p = 0; p < S::NQ; ++p) {
+          const int row = p * R + r, sz = S::W == 128 ? row & 7 : (row >> 1) & 3;
+          uint8_t *dst = sQ + c * S::NQpad * S::W + row * S::W + (((dd >> 4) ^ sz) << 4) + (dd & 15);
+          uint32_t word[(E + 3) / 4] = {};
+#pragma unroll
+          for (int e = 0; e < E; e += 2) {
+            const uint32_t v = to_e4m3x2(x[e], x[e + 1]);
+            word[e / 4] |= v << (8 * (e & 2));
+            if (p + 1 < S::NQ) {
+              const float2 b = __half22float2(from_e4m3x2(v));
+              x[e] = (x[e] - b.x) * 16.f;
+              x[e + 1] = (x[e + 1] - b.y) * 16.f;
+            }
+          }
+          if constexpr (E == 2) *reinterpret_cast<uint16_t *>(dst) = (uint16_t)word[0];
+          else if constexpr (E == 4) *reinterpret_cast<uint32_t *>(dst) = word[0];
+          else *reinterpret_cast<uint2 *>(dst) = make_uint2(word[0], word[E / 4 - 1]);
+        }
+        if (lane == 0) s_qf[qb + r] = scale_value(code) * (a.scale * kLog2e);
+      }
+      ptx::fence_proxy_async_smem();
+      ptx::mbar_arrive(&bars->q_full);
+    };
+    bool have = run.next();
+    if (have && run.last_block() > run.b0) prepare();
+    while (ok && have) {
       const int last = run.last_block();
       float m[R], l[R], o[S::CT][R];    // o is in units of exp2(m)
       float F[R];                       // what the pending block's O^T counts in units of exp2(m)
@@ -608,7 +587,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
         return true;
       };
       if (last > run.b0) {
-        if (!wait_warp(&bars->q_full[seg & 1], (uint32_t)((seg >> 1) & 1), abort_flag, a.err)) break;
+        // (the other warps' factors and counts too)
+        if (!wait_warp(&bars->q_full, (uint32_t)(seg & 1), abort_flag, a.err)) break;
         const float *qf = s_qf + (seg & 1) * 16;
         const int *ends = s_end + (seg & 1) * 16;
         int all = run.kv;               // keys that every row of the group sees
@@ -741,7 +721,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
           ok = false;
           break;
         }
-        qseg = seg++;
         // (s_l is written again only behind the next segment's first x_full)
 #pragma unroll
         for (int r = 0; r < R; ++r) l[r] = (s_l[r] + s_l[16 + r]) + (s_l[32 + r] + s_l[48 + r]);
@@ -749,7 +728,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
       const bool whole = run.b0 == 0 && run.b1 == run.nb;
       // 2 * place: the run begins inside the group; 2 * place + 1: it begins with it
       const size_t slot = 2 * (size_t)place + (run.b0 > 0 ? 0 : 1);
-      const long long *at = s_at + (qseg & 1) * 16;   // (whole groups have been through the Q warp)
+      if (!head_written && tid == 0) g.heads[place] = PartHead{run.s, hk, run.grp, run.b0};
+      head_written = true;
+      // the next segment's Q before this one's output: its first scores are computed meanwhile
+      const long long *at = s_at + (seg & 1) * 16;    // (a whole group has been prepared)
+      if (last > run.b0) ++seg;
+      have = run.next();
+      if (have && run.last_block() > run.b0) prepare();
       if (tid == 0) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -757,20 +742,24 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
           s_ml[2 * r + 1] = l[r];
         }
       }
+      if (whole) {
+        T *out = static_cast<T *>(a.out) + tid;
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        if (whole) {
+        for (int r = 0; r < R; ++r) {
           const long long row = at[r];
-          const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+          const float inv = l[r] == 0.f ? 0.f : ptx::rcp(l[r]);
           if (row >= 0)
 #pragma unroll
             for (int c = 0; c < S::CT; ++c)
-              if (D >= 128 || tid < D) store(static_cast<T *>(a.out) + row * D + c * 128 + tid, o[c][r] * inv);
-        } else {
+              if (D >= 128 || tid < D) store(out + row + c * 128, o[c][r] * inv);
+        }
+      } else {
+        float *po = g.o + slot * (R * D) + tid;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
 #pragma unroll
           for (int c = 0; c < S::CT; ++c)
-            if (D >= 128 || tid < D) g.o[(slot * R + r) * D + c * 128 + tid] = o[c][r];
-        }
+            if (D >= 128 || tid < D) po[r * D + c * 128] = o[c][r];
       }
       if (warp == 0) {
         __syncwarp();
@@ -780,15 +769,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
             g.ml[(slot * R + lane) * 2] = mr;
             g.ml[(slot * R + lane) * 2 + 1] = lr;
           } else if (a.lse != nullptr && at[lane] >= 0) {
-            a.lse[at[lane]] = lr == 0.f ? -INFINITY : (joined(mr) + log2f(lr)) * kLn2;
+            a.lse[at[lane] / D] = lr == 0.f ? -INFINITY : (joined(mr) + log2f(lr)) * kLn2;
           }
         }
         __syncwarp();
       }
-      if (last > run.b0) ptx::mbar_arrive(&bars->q_empty[qseg & 1]);
-      if (!head_written && tid == 0)
-        g.heads[place] = PartHead{run.s, hk, run.grp, run.b0};
-      head_written = true;
     }
     if (!head_written && tid == 0) g.heads[place].begin = 0;
   }
