@@ -140,10 +140,14 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volati
 }
 
 // Blocks of one sequence: groups of R rows per KV head, each of nb blocks (a
-// sequence without keys has one, empty, so that its rows are written).
+// sequence without keys has one, empty, so that its rows are written).  In the list
+// that is cut into runs a group counts kGroupCost blocks more, at its front: making Q's
+// parts and writing the output took 6,000 to 9,000 clocks beside 1,200 to 3,000 a block, and
+// without it the CTAs with many short groups took twice the average.
+constexpr int kGroupCost = 2;
 struct SeqWork {
   int groups, nb;
-  __device__ __forceinline__ int64_t blocks() const { return (int64_t)groups * nb; }
+  __device__ __forceinline__ int64_t blocks() const { return (int64_t)groups * (nb + kGroupCost); }
 };
 template <int R>
 __device__ __forceinline__ SeqWork seq_work(int q_len, int kv_len, int G, int q_limit) {
@@ -158,7 +162,7 @@ template <int R>
 struct Run {
   const AttendArgs *a;
   int n, G, q_limit;
-  int hk, s, grp_next, blk;
+  int hk, s, grp_next, blk;      // blk: place in the group, kGroupCost included
   int64_t left;
   // the current segment
   int q0, q_len, kv, grp, nb, b0, b1;
@@ -178,12 +182,12 @@ struct Run {
     }
     nb = w.nb;
     grp = grp_next++;
-    b0 = blk;
-    const int take = (int)(left < nb - blk ? left : nb - blk);
-    b1 = b0 + take;
-    left -= take;
+    const int end = nb + kGroupCost, stop = (int)(left < end - blk ? blk + left : end);
+    b0 = max(0, blk - kGroupCost);
+    b1 = max(0, stop - kGroupCost);
+    left -= stop - blk;
     blk = 0;
-    return true;
+    return b1 > b0;          // a run's end before a group's first block is no segment
   }
   // the segment's last block that any row sees, plus one (>= b0)
   __device__ __forceinline__ int last_block() const {
@@ -312,8 +316,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
   run.s = start.s;
   {
     const int nb = seq_work<R>(1, a.len.kv[start.s], G, INT_MAX).nb;
-    run.grp_next = (int)(start.off / nb);
-    run.blk = (int)(start.off - (int64_t)run.grp_next * nb);
+    run.grp_next = (int)(start.off / (nb + kGroupCost));
+    run.blk = (int)(start.off - (int64_t)run.grp_next * (nb + kGroupCost));
   }
   run.left = start.count;
 
@@ -909,7 +913,7 @@ int rows_grid(const rpa_dims &d, int32_t max_seqs, int32_t max_q, int R) {
 #undef RPA_Q8_CTAS
   // the same number of CTAs for every head, as many as are resident on 148 SMs;
   // fewer where the lengths cannot fill them
-  const double most = (double)seqs * groups * (double)((cap + BN - 1) / BN);
+  const double most = (double)seqs * groups * (double)((cap + BN - 1) / BN);   // (a run without a block is of no use)
   const int runs = std::max(1, 148 * ctas / d.num_kv_heads);
   return d.num_kv_heads * (int)std::max(1.0, std::min(most, (double)runs));
 }

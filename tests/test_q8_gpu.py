@@ -59,7 +59,8 @@ class Dev:
         dims = rb.make_dims(self.q, self.kc, self.table)
         size = rb.rpa_q8_workspace_size(dims, s, self.max_q)
         # poisoned, with a guard behind it that must keep its bytes
-        self.ws_all = torch.full((size + 256,), 255, dtype=torch.uint8, device="cuda")
+        # (bytes of a large positive integer: no word of it may be taken for a result)
+        self.ws_all = torch.full((size + 256,), 0x5A, dtype=torch.uint8, device="cuda")
         self.ws = self.ws_all[:size]
 
     @property
@@ -79,7 +80,7 @@ class Dev:
         t = self.pr.q.shape[0]
         R.check(self.out[:t], self.lse[:t], ref if ref is not None else R.attend(self.pr), what)
         assert (self.out[t:] == 77).all() and (self.lse[t:] == 77).all(), "rows behind the batch were written"
-        assert (self.ws_all[self.ws.numel():] == 255).all(), "written past the workspace"
+        assert (self.ws_all[self.ws.numel():] == 0x5A).all(), "written past the workspace"
 
 
 # --------------------------------------------------------------- write / read
@@ -253,7 +254,7 @@ def test_attend_loose_max_q(name):
     """max_q_len is a bound, not the longest: another choice of kernels."""
     dv = Dev(problem(name))
     dims = dv.rb.make_dims(dv.q, dv.kc, dv.table)
-    ws = torch.empty(dv.rb.rpa_q8_workspace_size(dims, dv.kv.numel(), 5000), dtype=torch.uint8, device="cuda")
+    ws = torch.full((dv.rb.rpa_q8_workspace_size(dims, dv.kv.numel(), 5000),), 0x5A, dtype=torch.uint8, device="cuda")
     dv.attend(max_q_len=5000, workspace=ws).checked(what=name)
 
 
