@@ -344,58 +344,100 @@ _lib.rpa_q8_attend.argtypes = [_P, _C, _P, _P, _P, _P, _i32, _i32, ctypes.c_floa
 _lib.rpa_q8_attend.restype = ctypes.c_int
 
 
+# the current stream's handle and device without building objects around them (a small
+# call is bound by this module's own time), where torch has these
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_E4M3, _E8M0, _I32 = torch.float8_e4m3fn, torch.float8_e8m0fnu, torch.int32
+_ROW_TYPES = {torch.float32: RPA_F32, torch.bfloat16: RPA_BF16}
+
+
+def _q8_tensor(name, t, index, dtype):
+    """Raises what is wrong with a tensor of a call on CUDA device `index`."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the token arrays on cuda:{index}")
+    raise ValueError(f"{name} must be contiguous")
+
+
 def _q8_common(rows, k_codes, v_codes, k_scales, v_scales, page_table, cu_lens, kv_lens, num_seqs, dev_flags, stream):
-    """Checks what the three calls share; returns the cache, the dims, the
-    list of device pointers (page_table, cu_lens, kv_lens, num_seqs), max_seqs,
-    the dev_flags and stream pointers, and the device of `rows`."""
-    device = rows.device
+    """Checks what the three calls share; returns the cache, the dims, max_seqs,
+    the dev_flags and stream pointers and the device index of `rows`."""
     if k_codes.dim() != 4 or rows.dim() != 3 or page_table.dim() != 2:
         raise ValueError("the codes have 4 dimensions, the token arrays 3 and page_table 2")
-    num_pages, page_size, hkv, d = k_codes.shape
-    for name, t in (("k_codes", k_codes), ("v_codes", v_codes)):
-        if t.shape != k_codes.shape or t.dtype != torch.float8_e4m3fn:
-            raise TypeError(f"{name} must be float8_e4m3fn {list(k_codes.shape)}, got {t.dtype} {list(t.shape)}")
-    for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
-        if t.shape != (num_pages, hkv, page_size) or t.dtype != torch.float8_e8m0fnu:
-            raise TypeError(f"{name} must be float8_e8m0fnu {[num_pages, hkv, page_size]}, got {t.dtype} "
-                            f"{list(t.shape)}")
+    shape = k_codes.shape
+    num_pages, page_size, hkv, d = shape
+    if v_codes.shape != shape:
+        raise TypeError(f"v_codes must have the shape of k_codes, {list(shape)}, got {list(v_codes.shape)}")
+    if k_scales.shape != (num_pages, hkv, page_size) or v_scales.shape != k_scales.shape:
+        raise TypeError(f"the scales must be {[num_pages, hkv, page_size]}, got {list(k_scales.shape)} and "
+                        f"{list(v_scales.shape)}")
+    total, heads, row_d = rows.shape
+    width = page_table.shape
     max_seqs = kv_lens.numel()
-    if cu_lens.numel() < max_seqs + 1 or num_seqs.numel() < 1 or page_table.shape[0] < max_seqs:
+    if cu_lens.numel() < max_seqs + 1 or num_seqs.numel() < 1 or width[0] < max_seqs:
         raise ValueError("cu_lens needs max_seqs + 1 entries, num_seqs one, page_table max_seqs rows")
-    if rows.shape[2] != d:
-        raise ValueError(f"head_dim {rows.shape[2]} of the token arrays is not the cache's {d}")
-    named = (("k_codes", k_codes), ("v_codes", v_codes), ("k_scales", k_scales), ("v_scales", v_scales),
-             ("page_table", page_table), ("cu_lens", cu_lens), ("kv_lens", kv_lens), ("num_seqs", num_seqs),
-             ("dev_flags", dev_flags))
-    for name, t in named:
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the token arrays on {device}")
-    cache = rpa_q8_cache(*(_dev(t, name) for name, t in named[:4]))
-    ptrs = [_dev(t, name, torch.int32) for name, t in named[4:8]]
-    dims = rpa_dims(num_q_heads=rows.shape[1], num_kv_heads=hkv, head_dim=d, page_size=page_size,
-                    num_pages=num_pages, max_pages_per_seq=page_table.shape[1], total_q_tokens=rows.shape[0],
-                    dtype=_dtype_code(rows))
+    if row_d != d:
+        raise ValueError(f"head_dim {row_d} of the token arrays is not the cache's {d}")
+    dtype = _ROW_TYPES.get(rows.dtype)
+    if dtype is None:
+        raise TypeError(f"unsupported dtype {rows.dtype}")
+    if k_codes.dtype is not _E4M3 or v_codes.dtype is not _E4M3:
+        raise TypeError(f"the codes must be {_E4M3}, got {k_codes.dtype} and {v_codes.dtype}")
+    if k_scales.dtype is not _E8M0 or v_scales.dtype is not _E8M0:
+        raise TypeError(f"the scales must be {_E8M0}, got {k_scales.dtype} and {v_scales.dtype}")
+    index = rows.get_device()
+    for t in (page_table, cu_lens, kv_lens, num_seqs):
+        if t.dtype is not _I32 or t.get_device() != index or not t.is_contiguous():
+            _q8_tensor("page_table, cu_lens, kv_lens or num_seqs", t, index, _I32)
+    for t in (rows, k_codes, v_codes, k_scales, v_scales):
+        if t.get_device() != index or not t.is_contiguous() or index < 0:
+            _q8_tensor("the token array, codes or scales", t, index, t.dtype)
+    flags = None
+    if dev_flags is not None:
+        if dev_flags.dtype is not _I32 or dev_flags.get_device() != index:
+            _q8_tensor("dev_flags", dev_flags, index, _I32)
+        flags = dev_flags.data_ptr()
+    cache = rpa_q8_cache(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr())
+    dims = rpa_dims(heads, hkv, d, page_size, num_pages, width[1], total, dtype)
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    sptr = ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
-    return cache, dims, ptrs, max_seqs, _dev(dev_flags, "dev_flags", torch.int32), sptr, device
-
-
-def _q8_call(name, device, *args):
-    """Calls the entry point with `device` current (its kernels launch there)."""
-    if device.index is not None and device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            rc = getattr(_lib, name)(*args)
+        stream = _raw_stream(index)
     else:
-        rc = getattr(_lib, name)(*args)
+        stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    return cache, dims, max_seqs, flags, stream, index
+
+
+def _q8_call(fn, index, *args):
+    """Calls the entry point with device `index` current (its kernels launch there)."""
+    if index == _current_device():
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args)
     if rc != RPA_OK:
-        raise RpaError(rc, name)
+        raise RpaError(rc, fn.__name__)
 
 
 def _same_rows(name, t, like):
-    if t.dtype != like.dtype or t.shape != like.shape or t.device != like.device:
+    if t.dtype is not like.dtype or t.shape != like.shape or t.get_device() != like.get_device():
         raise TypeError(f"{name} must be {like.dtype} {list(like.shape)} on {like.device}, "
                         f"got {t.dtype} {list(t.shape)} on {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _q8_io(fn, k, v, v_name, codes_scales, page_table, cu_lens, kv_lens, num_seqs, dev_flags, stream):
+    cache, dims, max_seqs, flags, sptr, index = _q8_common(k, *codes_scales, page_table, cu_lens, kv_lens, num_seqs,
+                                                           dev_flags, stream)
+    _same_rows(v_name, v, k)
+    if dims.num_q_heads != dims.num_kv_heads:
+        raise ValueError(f"the token arrays have {dims.num_q_heads} heads, the cache {dims.num_kv_heads}")
+    _q8_call(fn, index, k.data_ptr(), v.data_ptr(), ctypes.byref(cache), page_table.data_ptr(), cu_lens.data_ptr(),
+             kv_lens.data_ptr(), num_seqs.data_ptr(), max_seqs, ctypes.byref(dims), flags, sptr)
 
 
 def rpa_q8_write(k_new, v_new, k_codes, v_codes, k_scales, v_scales, page_table, cu_q_lens, kv_lens, num_seqs,
@@ -407,13 +449,8 @@ def rpa_q8_write(k_new, v_new, k_codes, v_codes, k_scales, v_scales, page_table,
     [max_seqs,max_pages], cu_q_lens [max_seqs+1], kv_lens [max_seqs] and
     num_seqs [1] int32.  dev_flags: optional int32 tensor of one element that
     receives the device error bits."""
-    cache, dims, ptrs, max_seqs, flags, sptr, device = _q8_common(
-        k_new, k_codes, v_codes, k_scales, v_scales, page_table, cu_q_lens, kv_lens, num_seqs, dev_flags, stream)
-    _same_rows("v_new", v_new, k_new)
-    if k_new.shape[1] != dims.num_kv_heads:
-        raise ValueError(f"k_new has {k_new.shape[1]} heads, the cache {dims.num_kv_heads}")
-    _q8_call("rpa_q8_write", device, _dev(k_new, "k_new"), _dev(v_new, "v_new"), ctypes.byref(cache), *ptrs,
-             max_seqs, ctypes.byref(dims), flags, sptr)
+    _q8_io(_lib.rpa_q8_write, k_new, v_new, "v_new", (k_codes, v_codes, k_scales, v_scales), page_table, cu_q_lens,
+           kv_lens, num_seqs, dev_flags, stream)
 
 
 def rpa_q8_read(k_out, v_out, k_codes, v_codes, k_scales, v_scales, page_table, cu_lens, kv_lens, num_seqs,
@@ -421,13 +458,8 @@ def rpa_q8_read(k_out, v_out, k_codes, v_codes, k_scales, v_scales, page_table, 
     """Calls rpa_q8_read: the last cu_lens[s+1] - cu_lens[s] cached positions
     of every sequence s into its rows of k_out / v_out [T,Hkv,D] (bf16 or
     fp32).  The other arguments are rpa_q8_write's."""
-    cache, dims, ptrs, max_seqs, flags, sptr, device = _q8_common(
-        k_out, k_codes, v_codes, k_scales, v_scales, page_table, cu_lens, kv_lens, num_seqs, dev_flags, stream)
-    _same_rows("v_out", v_out, k_out)
-    if k_out.shape[1] != dims.num_kv_heads:
-        raise ValueError(f"k_out has {k_out.shape[1]} heads, the cache {dims.num_kv_heads}")
-    _q8_call("rpa_q8_read", device, _dev(k_out, "k_out"), _dev(v_out, "v_out"), ctypes.byref(cache), *ptrs,
-             max_seqs, ctypes.byref(dims), flags, sptr)
+    _q8_io(_lib.rpa_q8_read, k_out, v_out, "v_out", (k_codes, v_codes, k_scales, v_scales), page_table, cu_lens,
+           kv_lens, num_seqs, dev_flags, stream)
 
 
 def rpa_q8_workspace_size(dims: rpa_dims, max_seqs: int, max_q_len: int) -> int:
@@ -449,13 +481,19 @@ def rpa_q8_attend(q, k_codes, v_codes, k_scales, v_scales, page_table, cu_q_lens
     q, out [T,Hq,D] bf16 or fp32, lse [T,Hq] float32 or None, max_q_len: an
     upper bound of the batch's q_lens, workspace: uint8 CUDA tensor of at least
     rpa_q8_workspace_size bytes.  The other arguments are rpa_q8_write's."""
-    cache, dims, ptrs, max_seqs, flags, sptr, device = _q8_common(
-        q, k_codes, v_codes, k_scales, v_scales, page_table, cu_q_lens, kv_lens, num_seqs, dev_flags, stream)
+    cache, dims, max_seqs, flags, sptr, index = _q8_common(q, k_codes, v_codes, k_scales, v_scales, page_table,
+                                                           cu_q_lens, kv_lens, num_seqs, dev_flags, stream)
     _same_rows("out", out, q)
-    if lse is not None and (tuple(lse.shape) != tuple(q.shape[:2]) or lse.device != device):
-        raise ValueError(f"lse must be {list(q.shape[:2])} on {device}")
-    if workspace.device != device:
-        raise ValueError(f"workspace is on {workspace.device}, the token arrays on {device}")
-    _q8_call("rpa_q8_attend", device, _dev(q, "q"), ctypes.byref(cache), *ptrs, max_seqs, int(max_q_len),
-             float(scale), int(bool(causal)), _dev(out, "out"), _dev(lse, "lse", torch.float32), ctypes.byref(dims),
-             _dev(workspace, "workspace", torch.uint8), workspace.numel(), flags, sptr)
+    lse_ptr = None
+    if lse is not None:
+        if lse.shape != q.shape[:2]:
+            raise ValueError(f"lse must be {list(q.shape[:2])}, got {list(lse.shape)}")
+        if lse.dtype is not torch.float32 or lse.get_device() != index or not lse.is_contiguous():
+            _q8_tensor("lse", lse, index, torch.float32)
+        lse_ptr = lse.data_ptr()
+    if workspace.dtype is not torch.uint8 or workspace.get_device() != index or not workspace.is_contiguous():
+        _q8_tensor("workspace", workspace, index, torch.uint8)
+    _q8_call(_lib.rpa_q8_attend, index, q.data_ptr(), ctypes.byref(cache), page_table.data_ptr(),
+             cu_q_lens.data_ptr(), kv_lens.data_ptr(), num_seqs.data_ptr(), max_seqs, int(max_q_len), float(scale),
+             int(bool(causal)), out.data_ptr(), lse_ptr, ctypes.byref(dims), workspace.data_ptr(), workspace.numel(),
+             flags, sptr)
