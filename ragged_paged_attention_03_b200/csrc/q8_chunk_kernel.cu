@@ -1,5 +1,5 @@
 // q8_chunk_kernel.cu -- attention over the 8-bit cache for chunks of query rows
-// (bf16, head_dim 64 / 128): bound by the tensor cores and the softmax.
+// (bf16): bound by the tensor cores and the softmax.
 //
 // Mathematics.  The query rows of one KV head, row = token i * G + head g, are
 // the M side (a KV head's G query heads share every key tile); S = Q K^T and
@@ -59,8 +59,8 @@ namespace q8 {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int BM = 128, BN = 128;   // rows of a tile, keys of a block
-constexpr int HN = 64;              // keys of a step: half a block
+constexpr int BM = 128;             // rows of a tile
+constexpr int HN = 64;              // keys of a step
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 6.0f;    // lazy rescale of O: weights reach 2^(6 + kBase)
@@ -72,15 +72,21 @@ constexpr int kSegSlots = 4;
 
 template <int D>
 struct Shape {
+  // head_dim 256: one tile, and blocks of 64 keys instead of 128 (TMEM holds one O of 256
+  // columns beside the scores, shared memory half as many keys)
+  static constexpr int NT = D == 256 ? 1 : 2;              // tiles of an item
+  static constexpr int BN = D == 256 ? 64 : 128;           // keys of a block
+  static constexpr int SPB = BN / HN;                      // steps of a block
+  static constexpr int ROWS = NT * BM;
   static constexpr int NSK = D == 64 ? 4 : 2, NSV = NSK;   // fp16 tiles
   static constexpr int NST = D == 64 ? 4 : 2;              // code tiles: K, V, K, V, ...
   static constexpr int kHalves = D / 64;
   static constexpr int kQBytes = kHalves * BM * 128;
   static constexpr int kKVBytes = kHalves * BN * 128;
   static constexpr int kCodes = BN * D;
-  static constexpr int kData = 2 * kQBytes + (NSK + NSV) * kKVBytes + NST * kCodes;
+  static constexpr int kData = NT * kQBytes + (NSK + NSV) * kKVBytes + NST * kCodes;
   static constexpr int kSmem = 1024 + kData + 2048;
-  static constexpr uint32_t kTmemCols = 512, kColO = 256;
+  static constexpr uint32_t kTmemCols = 512, kColO = NT * 128;
 };
 
 struct Bars {
@@ -104,7 +110,7 @@ struct Seg {
   int32_t whole;                 // the item begins and ends here
   int32_t pad[2];
 };
-constexpr int kSegUsers = 2 + 1 + 4 + 8;   // warps that release a slot: MMA, TMA of codes, converters, softmax
+template <int NT> constexpr int kSegUsers = NT + 1 + 4 + 4 * NT;   // warps that release a slot: MMA, TMA of codes, converters, softmax
 
 static_assert(1024 + sizeof(Bars) + 2 * kExpSlots * 4 + kSegSlots * sizeof(Seg) + 8 <= 2048, "control block");
 
@@ -117,8 +123,8 @@ struct Args {
   int32_t q_limit;       // sequences of at most this many new tokens are another kernel's
   int32_t tpt;           // tokens per tile: 128 / G
   PartHead *heads;       // [ctas]
-  float2 *ml;            // [2 * ctas][256] maximum (log2), sum
-  float4 *o;             // [2 * ctas][D / 4][256]
+  float2 *ml;            // [2 * ctas][ROWS] maximum (log2), sum
+  float4 *o;             // [2 * ctas][D / 4][ROWS]
 };
 
 // Waits for a phase, for at most kWaitLimitNs: false, with RPA_DEV_TIMEOUT raised,
@@ -142,30 +148,32 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, err));
 }
 
-// sum over i in [0, n) of floor((a i + b) / 128), a, b >= 0: by the quotients
-// and remainders of a and b, which leaves floor((a' i + b') / 128) with
-// a', b' < 128; its sum repeats every 128 terms.
-__device__ __forceinline__ int64_t floor_sum128(int64_t n, int64_t a, int64_t b) {
-  int64_t sum = (a >> 7) * (n * (n - 1) / 2) + (b >> 7) * n;
-  const int ar = (int)(a & 127), br = (int)(b & 127);
-  const int64_t turns = n >> 7;
-  const int rest = (int)(n & 127);
-  // i = 128 j + k: floor((ar i + br) / 128) = ar j + floor((ar k + br) / 128)
+// sum over i in [0, n) of floor((a i + b) / M), a, b >= 0: by the quotients and
+// remainders of a and b, which leaves floor((a' i + b') / M) with a', b' < M; its sum
+// repeats every M terms.
+template <int M>
+__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t a, int64_t b) {
+  int64_t sum = (a / M) * (n * (n - 1) / 2) + (b / M) * n;
+  const int ar = (int)(a % M), br = (int)(b % M);
+  const int64_t turns = n / M;
+  const int rest = (int)(n % M);
+  // i = M j + k: floor((ar i + br) / M) = ar j + floor((ar k + br) / M)
   int64_t whole = 0, part = 0;
   if (turns > 0)
 #pragma unroll 1
-    for (int k = 0; k < 128; ++k) whole += (ar * k + br) >> 7;
+    for (int k = 0; k < M; ++k) whole += (ar * k + br) / M;
 #pragma unroll 1
-  for (int k = 0; k < rest; ++k) part += (ar * k + br) >> 7;
-  return sum + turns * whole + (int64_t)ar * 128 * (turns * (turns - 1) / 2) + part + (int64_t)ar * turns * rest;
+  for (int k = 0; k < rest; ++k) part += (ar * k + br) / M;
+  return sum + turns * whole + (int64_t)ar * M * (turns * (turns - 1) / 2) + part + (int64_t)ar * turns * rest;
 }
 
 // The items of one sequence and KV head.  Item i holds tokens [i TT, (i + 1) TT)
-// and sees the first end(i) keys; it has max(1, ceil(end / 128)) blocks.  In the list
+// and sees the first end(i) keys; it has max(1, ceil(end / BN)) blocks.  In the list
 // that is cut into runs an item counts kItemCost blocks more, at its front: its Q and its
 // output take 12,000 clocks beside 5,000 a block, and runs of equal blocks took 370 to 467 us
 // where they held 9 and 22 items.
 constexpr int kItemCost = 2;
+template <int BN>
 struct SeqItems {
   int q_len, kv, TT, causal, items;
   __device__ __forceinline__ int end_of(int tokens) const {   // keys that token `tokens - 1` sees
@@ -183,34 +191,37 @@ struct SeqItems {
     // the first items whose last token sees no key have one block
     const int64_t none = c >= 0 ? 0 : min((int64_t)whole, -c / TT);
     int64_t sum = none;
-    if (whole > none) sum += floor_sum128(whole - none, TT, c + (none + 1) * TT + BN - 1);
+    if (whole > none) sum += floor_sum<BN>(whole - none, TT, c + (none + 1) * TT + BN - 1);
     if (n > whole) sum += blocks_of(n - 1);
     return sum + (int64_t)n * kItemCost;
   }
 };
-__device__ __forceinline__ SeqItems seq_items(int q_len, int kv, const Args &g) {
-  SeqItems w;
+template <int D>
+__device__ __forceinline__ SeqItems<Shape<D>::BN> seq_items(int q_len, int kv, const Args &g) {
+  SeqItems<Shape<D>::BN> w;
   w.q_len = q_len;
   w.kv = kv;
-  w.TT = 2 * g.tpt;
+  w.TT = Shape<D>::NT * g.tpt;
   w.causal = g.a.causal;
   w.items = q_len > g.q_limit ? (q_len + w.TT - 1) / w.TT : 0;
   return w;
 }
 
 // The CTA's run of blocks, one segment per item it touches.
+template <int D>
 struct Run {
+  static constexpr int SPB = Shape<D>::SPB;
   const Args *g;
   int n, s, hk, item, blk;       // blk: place in the item, kItemCost included
   int64_t left;
-  SeqItems w;
+  SeqItems<Shape<D>::BN> w;
   int q0, row0, b0, b1, nb;      // of the current segment: first token of the item, its blocks
   int nt[2];                     // steps (64 keys) of the segment that tile t takes part in
   int rows[2];                   // rows of tile t
 
   __device__ __forceinline__ void load() {
     q0 = g->a.len.cu[s];
-    w = seq_items(g->a.len.cu[s + 1] - q0, g->a.len.kv[s], *g);
+    w = seq_items<D>(g->a.len.cu[s + 1] - q0, g->a.len.kv[s], *g);
   }
   __device__ __forceinline__ bool next() {
     if (left <= 0) return false;
@@ -234,14 +245,14 @@ struct Run {
     const int G = g->a.hq / g->a.hkv;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const int tok = min(g->tpt, max(0, w.q_len - row0 - t * g->tpt));
+      const int tok = t < Shape<D>::NT ? min(g->tpt, max(0, w.q_len - row0 - t * g->tpt)) : 0;
       rows[t] = tok * G;
       const int vis = tok == 0 ? 0 : max(1, (w.end_of(row0 + t * g->tpt + tok) + HN - 1) / HN);
-      nt[t] = max(0, min(2 * b1, vis) - 2 * b0);
+      nt[t] = max(0, min(SPB * b1, vis) - SPB * b0);
     }
     return true;
   }
-  __device__ __forceinline__ int blocks() const { return (max(nt[0], nt[1]) + 1) >> 1; }
+  __device__ __forceinline__ int blocks() const { return (max(nt[0], nt[1]) + SPB - 1) / SPB; }
 };
 
 // 2^(e - top) as fp16 bits (0 below fp16's range; a byte of no key may lie above
@@ -265,12 +276,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const Args g) {
   using S = Shape<D>;
-  constexpr int NSK = S::NSK, NSV = S::NSV;
+  constexpr int NSK = S::NSK, NSV = S::NSV, NT = S::NT, BN = S::BN, SPB = S::SPB;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *sQ = base;
-  uint8_t *sK = sQ + 2 * S::kQBytes;
+  uint8_t *sK = sQ + NT * S::kQBytes;
   uint8_t *sV = sK + NSK * S::kKVBytes;
   uint8_t *sC = sV + NSV * S::kKVBytes;
   uint16_t *s_fac = reinterpret_cast<uint16_t *>(base + S::kData);   // [2][K, V][128] factors of a block's keys
@@ -293,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto finish = [] { asm volatile("griddepcontrol.wait;" ::: "memory"); };
   // ---- this CTA's run of blocks
   const Start start = find_start<kThreads>(a.len, cta, ctas, s_scan, [&](int q_len, int kv) {
-    const SeqItems w = seq_items(q_len, kv, g);
+    const auto w = seq_items<D>(q_len, kv, g);
     return w.before(w.items) * a.hkv;
   });
   if (start.count == 0) {
@@ -316,9 +327,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 4; ++i) {
       ptx::mbar_init(&bars->k_full[i], 128);
-      ptx::mbar_init(&bars->k_empty[i], 2);
+      ptx::mbar_init(&bars->k_empty[i], NT);
       ptx::mbar_init(&bars->v_full[i], 128);
-      ptx::mbar_init(&bars->v_empty[i], 2);
+      ptx::mbar_init(&bars->v_empty[i], NT);
     }
     for (int i = 0; i < 4; ++i) {
       ptx::mbar_init(&bars->c_full[i], 1);
@@ -331,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kExpSlots; ++i) ptx::mbar_init(&bars->e_full[i], 1);
     for (int i = 0; i < kSegSlots; ++i) {
       ptx::mbar_init(&bars->seg_full[i], 1);
-      ptx::mbar_init(&bars->seg_empty[i], kSegUsers);
+      ptx::mbar_init(&bars->seg_empty[i], kSegUsers<S::NT>);
     }
     ptx::mbar_init(&bars->drain[0], 1);
     ptx::mbar_init(&bars->drain[1], 1);
@@ -368,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= 12) {
     if (warp == 13) {
       // --------------------------------------------- the run, TMA of Q
-      Run run;
+      Run<D> run;
       run.g = &g;
       run.n = start.n;
       run.s = start.s;
@@ -411,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::mbar_arrive(&bars->seg_full[slot]);
         }
         __syncwarp();
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < NT; ++t) {
           if (!ok || !more || (t ? run.nt[1] : run.nt[0]) == 0) continue;
           const int u = t ? uses1 : uses0;
           if (u > 0) ok = wait_warp(&bars->q_empty[t], (uint32_t)((u - 1) & 1), abort_flag, err);
@@ -431,7 +442,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ----------------------------------- TMA of the codes, the scales
       const int br = a.p < BN ? a.p : BN;
       const int nload = BN / br;
-      constexpr int W = D < 128 ? D : 128;
       int gb = 0;
       bool ok = true;
       auto queue = [&](int v, bool load, uint32_t bytes, int hk, int row) -> bool {
@@ -440,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return false;
         ptx::mbar_arrive_expect_tx_elect(&bars->c_full[st], bytes);
         __syncwarp();
-        if (load) ptx::tma_load_3d(sC + st * S::kCodes + lane * br * W, v ? &tm_v : &tm_k, &bars->c_full[st], 0, hk, row);
+        if (load) ptx::tma_load_3d(sC + st * S::kCodes + lane * br * D, v ? &tm_v : &tm_k, &bars->c_full[st], 0, hk, row);
         __syncwarp();
         return true;
       };
@@ -455,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // keys 4 lane .. + 3 (-1: no key)
         auto page_at = [&](int j, int pos, bool use) -> int { return use && j < blocks && pos < kv ? pt[pos >> a.p_shift] : -1; };
         auto box_page = [&](int j) -> int { return page_at(j, (b0 + j) * BN + lane * br, lane < nload); };
-        auto key_page = [&](int j) -> int { return page_at(j, (b0 + j) * BN + lane * 4, true); };
+        auto key_page = [&](int j) -> int { return page_at(j, (b0 + j) * BN + lane * 4, lane < BN / 4); };
         auto scales_of = [&](int j, int pg, const uint8_t *src) -> uint32_t {
           if ((unsigned)pg >= (unsigned)a.num_pages) return 0;
           const int pos = (b0 + j) * BN + lane * 4;
@@ -505,8 +515,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             fv[k] = nan ? 0u : half_factor(wv ? ev : (int)((vs >> (8 * k)) & 255u), ev, false);
           }
           uint2 *dst = reinterpret_cast<uint2 *>(s_fac + fs * 2 * BN) + lane;
-          dst[0] = make_uint2(fk[0] | (fk[1] << 16), fk[2] | (fk[3] << 16));
-          dst[BN / 4] = make_uint2(fv[0] | (fv[1] << 16), fv[2] | (fv[3] << 16));
+          if (lane < BN / 4) dst[0] = make_uint2(fk[0] | (fk[1] << 16), fk[2] | (fk[3] << 16));
+          if (lane < BN / 4) dst[BN / 4] = make_uint2(fv[0] | (fv[1] << 16), fv[2] | (fv[3] << 16));
           if (lane == 0) {
             // free: the K tile of block gb - 1 is converted, so QK of block gb - 5 or a later one
             // is done for both tiles, and was issued behind the P of every block before it
@@ -531,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = queued - S::NST < 0 ? 0 : queued - S::NST; k < queued; ++k)
           ptx::mbar_wait(&bars->c_full[k % S::NST], (uint32_t)((k / S::NST) & 1));
       __syncwarp();
-    } else {
+    } else if (warp == 12 || NT == 2) {
       // ------------------------------------------------- MMA of one tile
       // A tile's scores of step n go to its S buffer n & 1, where P of step n replaces them;
       // QK(n + 2) follows PV(n) into the same buffer, so a tile's softmax has the scores of
@@ -550,13 +560,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int nt = sg->nt[t], nb = sg->blocks;
         done_seg();
 #pragma unroll 1
-        for (int vn = -2; vn < 2 * nb; ++vn) {
+        for (int vn = -2; vn < SPB * nb; ++vn) {
           const int kn = vn + 2;
           if (vn >= 0) {
             // (a block's tiles are waited for, and released, by both warps, whichever tile uses
             // them: an arrival of one warp must not count for the next block in the slot)
-            const int st = (gb + (vn >> 1)) % NSV;
-            if ((vn & 1) == 0 && !wait_warp(&bars->v_full[st], (uint32_t)(((gb + (vn >> 1)) / NSV) & 1), abort_flag, err)) {
+            const int st = (gb + vn / SPB) % NSV;
+            if (vn % SPB == 0 && !wait_warp(&bars->v_full[st], (uint32_t)(((gb + vn / SPB) / NSV) & 1), abort_flag, err)) {
               ok = false;
               break;
             }
@@ -567,22 +577,22 @@ __global__ void __launch_bounds__(kThreads, 1)
               ok = ok && wait_warp(&bars->p_full[t][buf], (uint32_t)(((gt + vn) >> 1) & 1), abort_flag, err);
               if (!ok) break;
               ptx::tc_fence_after();
-              ptx::umma_ts_x4_elect(tO, tS0 + buf * HN, dv0 + (uint64_t)((st * S::kKVBytes + (vn & 1) * HN * 128) >> 4),
+              ptx::umma_ts_x4_elect(tO, tS0 + buf * HN, dv0 + (uint64_t)((st * S::kKVBytes + (vn % SPB) * HN * 128) >> 4),
                                     idesc_pv, vn > 0 ? 1u : 0u);
               ptx::umma_commit_elect(&bars->pv_done[t][buf]);
             }
-            if (vn & 1) ptx::umma_commit_elect(&bars->v_empty[st]);
+            if (vn % SPB == SPB - 1) ptx::umma_commit_elect(&bars->v_empty[st]);
           }
-          const int st = (gb + (kn >> 1)) % NSK;
-          if ((kn & 1) == 0 && kn < 2 * nb) {
-            ok = wait_warp(&bars->k_full[st], (uint32_t)(((gb + (kn >> 1)) / NSK) & 1), abort_flag, err);
+          const int st = (gb + kn / SPB) % NSK;
+          if (kn % SPB == 0 && kn < SPB * nb) {
+            ok = wait_warp(&bars->k_full[st], (uint32_t)(((gb + kn / SPB) / NSK) & 1), abort_flag, err);
             if (ok && kn == 0 && nt > 0) ok = wait_warp(&bars->qc_full[t], (uint32_t)(ep & 1), abort_flag, err);
             if (!ok) break;
             ptx::tc_fence_after();
           }
           if (kn < nt) {
             const int buf = (gt + kn) & 1;
-            const uint64_t dk = dk0 + (uint64_t)((st * S::kKVBytes + (kn & 1) * HN * 128) >> 4);
+            const uint64_t dk = dk0 + (uint64_t)((st * S::kKVBytes + (kn % SPB) * HN * 128) >> 4);
 #pragma unroll
             for (int h = 0; h < S::kHalves; ++h)
               ptx::umma_ss_x4_elect(tS0 + buf * HN, dq + (uint64_t)((h * BM * 128) >> 4),
@@ -590,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::umma_commit_elect(&bars->s_full[t][buf]);
             if (kn + 1 == nt) ptx::umma_commit_elect(&bars->q_empty[t]);
           }
-          if ((kn & 1) && kn < 2 * nb) ptx::umma_commit_elect(&bars->k_empty[st]);
+          if (kn % SPB == SPB - 1 && kn < SPB * nb) ptx::umma_commit_elect(&bars->k_empty[st]);
         }
         gb += nb;
         gt += nt;
@@ -608,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int cw = warp - 8, lrow = lane / LPR, lcol = lane % LPR;
     const int row0 = lrow * (4 * NU) + cw * NU;
     // the two 16-byte chunks of a lane's values, in the order that hits no bank twice
-    const int swp = D == 64 ? lrow & 1 : lcol >> 2;
+    const int swp = D == 64 ? lrow & 1 : (lcol >> 2) & 1;
     const int c0 = 2 * (lcol & 3) + swp, c1 = c0 ^ 1;
     const uint32_t src0 = (uint32_t)(row0 * D + lcol * 16 + swp * 8);
     const uint32_t dst0 = (uint32_t)((lcol >> 2) * BN * 128 + row0 * 128);
@@ -672,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) ptx::mbar_arrive(&bars->f_empty[gb & 1]);
       }
     }
-  } else {
+  } else if (warp < 4 * NT) {
     // ------------------------------------------------------ softmax, output
     const int t = warp >> 2, row = tid & 127;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -747,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (have && ok) {
       if (c.nt == 0) {
         // no block of this segment is seen by the tile: an empty part
-        if (!c.whole && c.mine) g.ml[c.slot * 256 + t * 128 + row] = make_float2(-INFINITY, 0.f);
+        if (!c.whole && c.mine) g.ml[c.slot * S::ROWS + t * 128 + row] = make_float2(-INFINITY, 0.f);
         gb += c.nb;
         have = take(c);
         continue;
@@ -760,9 +770,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY, l = 0.f;                   // l counts 2^kBase per unit weight
       int evr = 0;                                    // O is in units of 2^(m + evr - kBase)
       for (int j = 0; j < nt; ++j) {                  // steps
-        const int blk = gb + (j >> 1), eslot = blk % kExpSlots, buf = (gt + j) & 1;
+        const int blk = gb + j / SPB, eslot = blk % kExpSlots, buf = (gt + j) & 1;
         const uint32_t tS = lane_base + (uint32_t)(t * 128 + buf * HN);
-        if ((j & 1) == 0) {                           // a new block's scales
+        if (j % SPB == 0) {                           // a new block's scales
           ok = wait_warp(&bars->e_full[eslot], (uint32_t)((blk / kExpSlots) & 1), abort_flag, err);
           ek = s_exp[eslot * 2];
           ev = s_exp[eslot * 2 + 1];
@@ -970,14 +980,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::st_global_hint8(out + 8 * i, o2, once);
           }
         } else {
-          float4 *po = g.o + (c.slot * (D / 4) + cc / 4) * 256 + t * 128 + row;
+          float4 *po = g.o + (c.slot * (D / 4) + cc / 4) * S::ROWS + t * 128 + row;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) po[i * 256] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          for (int i = 0; i < 8; ++i) po[i * S::ROWS] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
       }
       if (c.mine) {
         if (!c.whole)
-          g.ml[c.slot * 256 + t * 128 + row] = make_float2(m, l);
+          g.ml[c.slot * S::ROWS + t * 128 + row] = make_float2(m, l);
         else if (a.lse != nullptr)
           a.lse[c.at] = l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l) - kBase) * kLn2;
       }
@@ -992,11 +1002,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the parts of an item that several runs share (see the row-group
-// kernel's).  Block 16 i + y joins 16 of the item's 256 rows, 16 lanes a row.
+// kernel's).  A block joins 16 of an item's rows, 16 lanes a row.
 template <int D>
 __global__ void __launch_bounds__(256) combine_kernel(const Args g) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int i = blockIdx.x >> 4, ctas = gridDim.x >> 4;
+  constexpr int ROWS = Shape<D>::ROWS, PER = ROWS / 16;      // blocks per item
+  const int i = blockIdx.x / PER, ctas = gridDim.x / PER;
   const PartHead h = g.heads[i];
   if (h.begin <= 0) return;
   auto same = [&](const PartHead &p) { return p.begin > 0 && p.seq == h.seq && p.hk == h.hk && p.item == h.item; };
@@ -1004,15 +1015,15 @@ __global__ void __launch_bounds__(256) combine_kernel(const Args g) {
   const AttendArgs &a = g.a;
   const int G = a.hq / a.hkv;
   const int q0 = a.len.cu[h.seq], q_len = a.len.cu[h.seq + 1] - q0;
-  const int r = (blockIdx.x & 15) * 16 + (threadIdx.x & 15), t = r >> 7, row = r & 127;
-  const int tok = row / G, tk = (2 * h.item + t) * g.tpt + tok;
+  const int r = (blockIdx.x % PER) * 16 + (threadIdx.x & 15), t = r >> 7, row = r & 127;
+  const int tok = row / G, tk = (Shape<D>::NT * h.item + t) * g.tpt + tok;
   if (tok >= g.tpt || tk >= q_len) return;
   int end = i + 1;
   while (end < ctas && same(g.heads[end])) ++end;
   const int parts = end - i + 1;
   auto slot = [&](int k) { return (size_t)(k == 0 ? 2 * (i - 1) + 1 : 2 * (i + k - 1)); };
   float M = -INFINITY, l = 0.f;
-  for (int k = 0; k < parts; ++k) M = fmaxf(M, g.ml[slot(k) * 256 + r].x);
+  for (int k = 0; k < parts; ++k) M = fmaxf(M, g.ml[slot(k) * ROWS + r].x);
   constexpr int NC = D / 64;                 // float4 pieces per thread
   const int c0 = threadIdx.x >> 4;
   float4 acc[NC];
@@ -1020,10 +1031,10 @@ __global__ void __launch_bounds__(256) combine_kernel(const Args g) {
   for (int c = 0; c < NC; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
   for (int k = 0; k < parts; ++k) {
-    const float2 ml = g.ml[slot(k) * 256 + r];
+    const float2 ml = g.ml[slot(k) * ROWS + r];
     float4 v[NC];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) v[c] = g.o[(slot(k) * (D / 4) + c * 16 + c0) * 256 + r];
+    for (int c = 0; c < NC; ++c) v[c] = g.o[(slot(k) * (D / 4) + c * 16 + c0) * ROWS + r];
     if (ml.y == 0.f) continue;               // saw no key: nothing there
     const float wt = ml.x == M ? 1.f : ptx::ex2((ml.x == -INFINITY ? 0.f : ml.x) - (M == -INFINITY ? 0.f : M));
     l = fmaf(wt, ml.y, l);
@@ -1061,7 +1072,7 @@ cudaError_t launch_t(const AttendArgs &a, int q_limit, int total_q, int grid, ui
   CUtensorMap tk, tv;
   const uint64_t cdims[3] = {(uint64_t)D, (uint64_t)a.hkv, (uint64_t)a.num_pages * a.p};
   const uint64_t cstrides[2] = {(uint64_t)D, (uint64_t)a.hkv * D};
-  const uint32_t cbox[3] = {(uint32_t)D, 1, (uint32_t)(a.p < BN ? a.p : BN)};
+  const uint32_t cbox[3] = {(uint32_t)D, 1, (uint32_t)(a.p < S::BN ? a.p : S::BN)};
   if (!make_tmap_u8_3d(&tk, a.c.k, cdims, cstrides, cbox, false) ||
       !make_tmap_u8_3d(&tv, a.c.v, cdims, cstrides, cbox, false))
     return cudaErrorInvalidValue;
@@ -1076,16 +1087,20 @@ cudaError_t launch_t(const AttendArgs &a, int q_limit, int total_q, int grid, ui
   if (e != cudaSuccess) return e;
   e = launch_behind(kern, grid, kThreads, S::kSmem, stream, tq, tk, tv, g);
   if (e != cudaSuccess || grid == 1) return e;
-  return launch_behind(combine_kernel<D>, 16 * grid, 256, 0, stream, g);
+  return launch_behind(combine_kernel<D>, S::ROWS / 16 * grid, 256, 0, stream, g);
 }
 
 }  // namespace
 
-bool chunk_takes(const rpa_dims &d) { return d.dtype == RPA_BF16 && d.head_dim <= 128; }
+bool chunk_takes(const rpa_dims &d) { return d.dtype == RPA_BF16; }
+
+// Rows of an item and keys of a block (Shape's).
+static int item_tiles(int D) { return D == 256 ? Shape<256>::NT : Shape<128>::NT; }
+static int block_keys(int D) { return D == 256 ? Shape<256>::BN : Shape<128>::BN; }
 
 int chunk_grid(const rpa_dims &d, int32_t max_seqs, int32_t max_q) {
   const int64_t cap = (int64_t)d.max_pages_per_seq * d.page_size;
-  const int TT = 2 * (BM / (d.num_q_heads / d.num_kv_heads));
+  const int TT = item_tiles(d.head_dim) * (BM / (d.num_q_heads / d.num_kv_heads)), BN = block_keys(d.head_dim);
   const int64_t seqs = std::min<int64_t>(max_seqs, d.total_q_tokens);
   const double most = (double)seqs * d.num_kv_heads * (double)((max_q + TT - 1) / TT) * (double)((cap + BN - 1) / BN);
   return (int)std::max(1.0, std::min(most, 148.0));
@@ -1096,8 +1111,9 @@ ChunkLayout chunk_layout(int grid, int D) {
   auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
   w.heads = 0;
   w.ml = up((int64_t)grid * sizeof(PartHead));
-  w.o = up(w.ml + (int64_t)grid * 2 * 256 * 8);
-  w.total = up(w.o + (int64_t)grid * 2 * 256 * D * 4);
+  const int64_t rows = (int64_t)grid * 2 * item_tiles(D) * BM;
+  w.o = up(w.ml + rows * 8);
+  w.total = up(w.o + rows * D * 4);
   return w;
 }
 
@@ -1107,6 +1123,7 @@ cudaError_t launch_chunk(const AttendArgs &a, const rpa_dims &d, int32_t max_seq
   switch (d.head_dim) {
     case 64: return launch_t<64>(a, q_limit, d.total_q_tokens, grid, ws, stream);
     case 128: return launch_t<128>(a, q_limit, d.total_q_tokens, grid, ws, stream);
+    case 256: return launch_t<256>(a, q_limit, d.total_q_tokens, grid, ws, stream);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -53,7 +53,7 @@ RowsLayout rows_layout(int grid, int R, int D);
 cudaError_t launch_rows(const AttendArgs &a, const rpa_dims &d, int32_t max_seqs, int32_t max_q, int32_t q_limit,
                         uint8_t *ws, cudaStream_t stream);
 
-// Chunks of query rows (bf16, head_dim 64 / 128).  Sequences with q_len <=
+// Chunks of query rows (bf16).  Sequences with q_len <=
 // q_limit are left out.
 bool chunk_takes(const rpa_dims &d);
 int chunk_grid(const rpa_dims &d, int32_t max_seqs, int32_t max_q);
