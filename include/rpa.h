@@ -458,8 +458,8 @@ RPA_API int rpa_host_groups(const int32_t *cu_q_lens, int32_t num_seqs,
  *
  * dims->dtype is the type of the arrays outside the cache (RPA_BF16 or
  * RPA_F32); head_dim, page_size and G are limited as in rpa_forward.  Token
- * arrays, codes and scales must be 16-byte aligned (RPA_ERR_INVALID_ARG
- * otherwise).
+ * arrays must be 32-byte, codes and scales 16-byte aligned
+ * (RPA_ERR_INVALID_ARG otherwise).
  * dev_flags: device uint32 that receives RPA_DEV_* bits (OR-ed in, never
  * cleared), or NULL to drop them.  Lengths that break a rule set
  * RPA_DEV_BAD_LENGTHS and the call writes nothing else; a page-table entry
@@ -530,7 +530,7 @@ RPA_API int rpa_q8_workspace_size(const rpa_dims *dims, int32_t max_seqs,
  *   rpa_q8_workspace_size bytes, else RPA_ERR_WORKSPACE.  Its contents need no
  *   initialisation and mean nothing after the call; calls that share one must
  *   be ordered on the device (two graphs that may run at once need two).
- * out must be 32-byte aligned.  out and lse must not overlap any input.
+ * out and lse must not overlap any input.
  */
 RPA_API int rpa_q8_attend(const void *q, const rpa_q8_cache *cache,
                           const int32_t *page_table, const int32_t *cu_q_lens,

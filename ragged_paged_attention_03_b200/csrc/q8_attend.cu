@@ -78,7 +78,7 @@ extern "C" RPA_API int rpa_q8_attend(const void *q, const rpa_q8_cache *cache, c
   if (!q || !cache || !cache->k_codes || !cache->v_codes || !cache->k_scales || !cache->v_scales || !page_table ||
       !cu_q_lens || !kv_lens || !num_seqs || !out || !workspace)
     return RPA_ERR_INVALID_ARG;
-  if (!aligned16(q) || reinterpret_cast<uintptr_t>(out) % 32 != 0 || !aligned16(cache->k_codes) || !aligned16(cache->v_codes) ||
+  if (!aligned32(q) || !aligned32(out) || !aligned16(cache->k_codes) || !aligned16(cache->v_codes) ||
       !aligned16(cache->k_scales) || !aligned16(cache->v_scales))
     return RPA_ERR_INVALID_ARG;
   const AttendLayout w = attend_layout(*dims, max_seqs, max_q_len);

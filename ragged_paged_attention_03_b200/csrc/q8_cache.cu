@@ -2,10 +2,13 @@
 // (rpa_q8_write) and reading cached rows back (rpa_q8_read).
 //
 // Both are one pass over the rows and bound by memory: a row of D values
-// moves D * sizeof(T) + D + 1 bytes.  D / 16 neighbouring lanes share a row,
-// each with 16 of its values in 16-byte pieces that stay in registers between
-// the row's maximum (shuffles among those lanes) and the rounding, so every
-// value is read once; K and V of a row are in flight together.
+// moves D * sizeof(T) + D + 1 bytes.  D / 16 neighbouring lanes share a row, each
+// with 16 values next to each other: 32-byte loads or stores of T (two for fp32) and
+// 16-byte ones of codes.  The values stay in registers between the row's maximum
+// (shuffles among those lanes) and the rounding, so every value is read once; K and V of
+// a row are in flight together.  A warp's rows are neighbouring tokens of one head, so
+// that their scales, single bytes, share a sector, and neighbouring warps take the
+// heads, so that together they read what lies together.
 #include <algorithm>
 #include <cuda_runtime.h>
 
@@ -19,7 +22,7 @@ namespace q8 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kCuCap = 1024;   // sequences whose offsets are kept in shared memory
+constexpr int kLenCap = 512;    // sequences whose lengths are kept in shared memory
 
 struct IoArgs {
   void *k, *v;                 // [T, Hkv, D] rows outside the cache
@@ -30,139 +33,127 @@ struct IoArgs {
   int32_t hkv, p, p_shift, num_pages, max_pages;
 };
 
-// 16 bytes of T as fp32 values and back (rounded to nearest-even).
-template <typename T> struct Piece;
-template <> struct Piece<float> {
-  static constexpr int E = 4;
-  static __device__ __forceinline__ void unpack(const uint4 &u, float (&f)[4]) {
-    f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y);
-    f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
-  }
-  static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-  }
-};
-template <> struct Piece<__nv_bfloat16> {
-  static constexpr int E = 8;
-  static __device__ __forceinline__ void unpack(const uint4 &u, float (&f)[8]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// 16 values of T next to each other, as 32-bit words.
+template <typename T> constexpr int kWords = 4 * (int)sizeof(T);
+template <typename T>
+__device__ __forceinline__ void load16(const T *p, uint32_t (&w)[kWords<T>]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
-  static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
-    uint32_t w[4];
+  for (int i = 0; i < kWords<T>; i += 8)
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]), "=r"(w[i + 4]), "=r"(w[i + 5]),
+                   "=r"(w[i + 6]), "=r"(w[i + 7])
+                 : "l"(reinterpret_cast<const uint32_t *>(p) + i));
+}
+template <typename T>
+__device__ __forceinline__ void store16(T *p, const uint32_t (&w)[kWords<T>]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
-};
+  for (int i = 0; i < kWords<T>; i += 8)
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(reinterpret_cast<uint32_t *>(p) + i),
+                 "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]), "r"(w[i + 5]), "r"(w[i + 6]),
+                 "r"(w[i + 7])
+                 : "memory");
+}
+// value i of the 16
+__device__ __forceinline__ float value(const uint32_t (&w)[16], int i) { return __uint_as_float(w[i]); }
+__device__ __forceinline__ float value(const uint32_t (&w)[8], int i) {
+  return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+}
+__device__ __forceinline__ void put(uint32_t (&w)[16], int i, float a, float b) {
+  w[i] = __float_as_uint(a);
+  w[i + 1] = __float_as_uint(b);
+}
+__device__ __forceinline__ void put(uint32_t (&w)[8], int i, float a, float b) {
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i / 2]) : "f"(b), "f"(a));
+}
 
 template <typename T, int D, bool WRITE>
 __global__ void __launch_bounds__(kThreads) io_kernel(const IoArgs a) {
-  constexpr int E = Piece<T>::E;      // values per 16-byte piece
-  constexpr int NP = 16 / E;          // pieces per lane
   constexpr int LPR = D / 16;         // lanes per row
-  __shared__ int32_t s_cu[kCuCap + 1];
+  constexpr int RW = 32 / LPR;        // rows (tokens) per warp
+  __shared__ int32_t s_cu[kLenCap + 1], s_kv[kLenCap];
   const int n = checked_seqs(a.len);
   if (n < 0) {
     if (blockIdx.x == 0 && threadIdx.x == 0) raise(a.err, RPA_DEV_BAD_LENGTHS);
     return;
   }
   if (n == 0) return;
-  const int32_t *cu = a.len.cu;
-  if (n <= kCuCap) {
-    for (int i = threadIdx.x; i <= n; i += kThreads) s_cu[i] = a.len.cu[i];
+  const int32_t *cu = a.len.cu, *kv = a.len.kv;
+  if (n <= kLenCap) {
+    for (int i = threadIdx.x; i <= n; i += kThreads) {
+      s_cu[i] = a.len.cu[i];
+      if (i < n) s_kv[i] = a.len.kv[i];
+    }
     __syncthreads();
     cu = s_cu;
+    kv = s_kv;
   }
-  const int64_t rows = (int64_t)cu[n] * a.hkv;
-  const int sub = threadIdx.x % LPR;
-  const int64_t step = (int64_t)gridDim.x * (kThreads / LPR);
-  // a row's lanes are neighbours in one warp and leave the loop together
-  const unsigned lanes = LPR == 32 ? 0xffffffffu : ((1u << LPR) - 1u) << ((threadIdx.x & 31) / LPR * LPR);
-  for (int64_t r = (int64_t)blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR; r < rows; r += step) {
-    const int t = (int)(r / a.hkv);
-    const int h = (int)(r - (int64_t)t * a.hkv);
-    const size_t row = (size_t)r * D + sub * E;
-    uint4 x[2][NP];
+  const int total = cu[n];
+  const int lane = threadIdx.x & 31, sub = lane % LPR;
+  // a row's lanes are neighbours in one warp and take the same way
+  const unsigned lanes = LPR == 32 ? 0xffffffffu : ((1u << LPR) - 1u) << (lane / LPR * LPR);
+  const int64_t tasks = (int64_t)((total + RW - 1) / RW) * a.hkv;
+  const int64_t step = (int64_t)gridDim.x * (kThreads / 32);
+  for (int64_t task = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; task < tasks; task += step) {
+    const int tg = (int)(task / a.hkv), h = (int)(task - (int64_t)tg * a.hkv);
+    const int t = tg * RW + lane / LPR;
+    if (t >= total) continue;
+    const size_t row = ((size_t)t * a.hkv + h) * D + sub * 16;
+    uint32_t x[2][kWords<T>];
     if (WRITE) {
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        x[0][i] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const T *>(a.k) + row + i * (LPR * E)));
-        x[1][i] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const T *>(a.v) + row + i * (LPR * E)));
-      }
+      load16(static_cast<const T *>(a.k) + row, x[0]);
+      load16(static_cast<const T *>(a.v) + row, x[1]);
     }
     const int s = seq_of(cu, n, t);
-    const int pos = a.len.kv[s] - cu[s + 1] + t;   // kv_len - q_len + (t - cu[s])
+    const int pos = kv[s] - cu[s + 1] + t;         // kv_len - q_len + (t - cu[s])
     const int page = a.page_table[(size_t)s * a.max_pages + (pos >> a.p_shift)];
     const bool ok = page >= 0 && page < a.num_pages;
     if (!ok && sub == 0) raise(a.err, RPA_DEV_BAD_PAGE);
     const int slot = pos & (a.p - 1);
-    const size_t crow = (((size_t)(ok ? page : 0) * a.p + slot) * a.hkv + h) * D + sub * E;
+    const size_t crow = (((size_t)(ok ? page : 0) * a.p + slot) * a.hkv + h) * D + sub * 16;
     const size_t srow = ((size_t)(ok ? page : 0) * a.hkv + h) * a.p + slot;
     if (WRITE) {
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        float f[NP][E];
-        uint32_t amax = 0;
+      for (int v = 0; v < 2; ++v) {
         // |x| as integers: ordered like the values, with infinities and NaN on top
+        uint32_t amax = 0;
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          Piece<T>::unpack(x[kv][i], f[i]);
-#pragma unroll
-          for (int j = 0; j < E; ++j) amax = max(amax, __float_as_uint(f[i][j]) & 0x7fffffffu);
-        }
+        for (int i = 0; i < 16; ++i) amax = max(amax, __float_as_uint(value(x[v], i)) & 0x7fffffffu);
 #pragma unroll
         for (int o = 1; o < LPR; o <<= 1) amax = max(amax, __shfl_xor_sync(lanes, amax, o));
         const uint32_t code = scale_code(amax);
         const float inv = code == kScaleNan ? 0.f : inverse_scale(code);
         if (!ok) continue;
-        uint8_t *dst = (kv ? a.c.v : a.c.k) + crow;
+        uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          uint32_t w[E / 4];
-#pragma unroll
-          for (int j = 0; j < E / 4; ++j)
-            w[j] = code == kScaleNan ? 0u : to_e4m3x2(f[i][4 * j] * inv, f[i][4 * j + 1] * inv) |
-                                                (to_e4m3x2(f[i][4 * j + 2] * inv, f[i][4 * j + 3] * inv) << 16);
-          if (E == 8) *reinterpret_cast<uint2 *>(dst + i * (LPR * E)) = make_uint2(w[0], w[E / 4 - 1]);
-          else *reinterpret_cast<uint32_t *>(dst + i * (LPR * E)) = w[0];
-        }
-        if (sub == 0) (kv ? a.c.vs : a.c.ks)[srow] = (uint8_t)code;
+        for (int i = 0; i < 4; ++i)
+          w[i] = code == kScaleNan
+                     ? 0u
+                     : to_e4m3x2(value(x[v], 4 * i) * inv, value(x[v], 4 * i + 1) * inv) |
+                           (to_e4m3x2(value(x[v], 4 * i + 2) * inv, value(x[v], 4 * i + 3) * inv) << 16);
+        *reinterpret_cast<uint4 *>((v ? a.c.v : a.c.k) + crow) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (sub == 0) (v ? a.c.vs : a.c.ks)[srow] = (uint8_t)code;
       }
     } else {
-      uint2 c[2][NP];
+      uint4 c[2];
       uint32_t sc[2];
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        const uint8_t *src = (kv ? a.c.v : a.c.k) + crow;
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          if (E == 8) c[kv][i] = *reinterpret_cast<const uint2 *>(src + i * (LPR * E));
-          else c[kv][i].x = *reinterpret_cast<const uint32_t *>(src + i * (LPR * E));
-        }
-        sc[kv] = (kv ? a.c.vs : a.c.ks)[srow];
+      for (int v = 0; v < 2; ++v) {
+        c[v] = *reinterpret_cast<const uint4 *>((v ? a.c.v : a.c.k) + crow);
+        sc[v] = (v ? a.c.vs : a.c.ks)[srow];
       }
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
+      for (int v = 0; v < 2; ++v) {
         // a page outside the pool reads as zeros
-        const float scale = ok ? scale_value(sc[kv]) : 0.f;
-        T *dst = static_cast<T *>(kv ? a.v : a.k) + row;
+        const float scale = ok ? scale_value(sc[v]) : 0.f;
+        const uint32_t w[4] = {c[v].x, c[v].y, c[v].z, c[v].w};
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          float f[E];
-#pragma unroll
-          for (int j = 0; j < E / 4; ++j) {
-            float g[4];
-            e4m3x4_to_f32(j == 0 ? c[kv][i].x : c[kv][i].y, g);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) f[4 * j + e] = ok ? g[e] * scale : 0.f;
-          }
-          __stcs(reinterpret_cast<uint4 *>(dst + i * (LPR * E)), Piece<T>::pack(f));
+        for (int i = 0; i < 4; ++i) {
+          float g[4];
+          e4m3x4_to_f32(ok ? w[i] : 0u, g);
+          put(x[v], 4 * i, g[0] * scale, g[1] * scale);
+          put(x[v], 4 * i + 2, g[2] * scale, g[3] * scale);
         }
+        store16(static_cast<T *>(v ? a.v : a.k) + row, x[v]);
       }
     }
   }
@@ -179,7 +170,7 @@ int io_call(void *k, void *v, const rpa_q8_cache *cache, const int32_t *page_tab
   if (!k || !v || !cache || !cache->k_codes || !cache->v_codes || !cache->k_scales || !cache->v_scales ||
       !page_table || !cu || !kv || !num_seqs)
     return RPA_ERR_INVALID_ARG;
-  if (!aligned16(k) || !aligned16(v) || !aligned16(cache->k_codes) || !aligned16(cache->v_codes) ||
+  if (!aligned32(k) || !aligned32(v) || !aligned16(cache->k_codes) || !aligned16(cache->v_codes) ||
       !aligned16(cache->k_scales) || !aligned16(cache->v_scales))
     return RPA_ERR_INVALID_ARG;
   IoArgs a{};
@@ -195,8 +186,8 @@ int io_call(void *k, void *v, const rpa_q8_cache *cache, const int32_t *page_tab
   a.num_pages = d->num_pages;
   a.max_pages = d->max_pages_per_seq;
   // enough blocks to fill 148 SMs at 8 blocks each; longer batches loop
-  const int64_t rows = (int64_t)d->total_q_tokens * d->num_kv_heads;
-  const int64_t per = kThreads / (d->head_dim / 16);
+  const int64_t per = (512 / d->head_dim) * (kThreads / 32);     // rows of a block's warps
+  const int64_t rows = ((int64_t)d->total_q_tokens + 31) / 32 * 32 * d->num_kv_heads;
   const unsigned grid = (unsigned)std::min<int64_t>((rows + per - 1) / per, 148 * 8);
 #define RPA_Q8_IO(DD)                                                                                \
   case DD:                                                                                           \

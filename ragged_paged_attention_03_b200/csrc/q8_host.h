@@ -10,6 +10,8 @@ namespace q8 {
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+inline bool aligned32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; }
+
 inline int log2_of(int32_t pow2) {
   int s = 0;
   while ((1 << s) < pow2) ++s;

@@ -79,6 +79,7 @@ def test_null_cache_parts(rb, i):
 def test_misaligned(rb):
     for name in ("rpa_q8_write", "rpa_q8_read"):
         assert io(rb, name, k=FAKE + 8) == 1
+        assert io(rb, name, v=FAKE + 16) == 1
         assert io(rb, name, cache=(FAKE, FAKE + 4, FAKE, FAKE)) == 1
     assert attend(rb, q=FAKE + 2) == 1
     assert attend(rb, out=FAKE + 8) == 1
