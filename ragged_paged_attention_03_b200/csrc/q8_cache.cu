@@ -13,6 +13,7 @@
 #include <cuda_runtime.h>
 
 #include "host_common.h"
+#include "ptx.cuh"
 #include "q8_common.cuh"
 #include "q8_host.h"
 #include "rpa.h"
@@ -53,17 +54,37 @@ __device__ __forceinline__ void store16(T *p, const uint32_t (&w)[kWords<T>]) {
                  "r"(w[i + 7])
                  : "memory");
 }
-// value i of the 16
-__device__ __forceinline__ float value(const uint32_t (&w)[16], int i) { return __uint_as_float(w[i]); }
-__device__ __forceinline__ float value(const uint32_t (&w)[8], int i) {
-  return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+// The fp32 bits of the largest |x|: compared as integers, with infinities and NaN on top,
+// or two bf16 at a time (a NaN stays).
+__device__ __forceinline__ uint32_t absmax(const uint32_t (&w)[16]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = max(m, w[i] & 0x7fffffffu);
+  return m;
 }
-__device__ __forceinline__ void put(uint32_t (&w)[16], int i, float a, float b) {
-  w[i] = __float_as_uint(a);
-  w[i + 1] = __float_as_uint(b);
+__device__ __forceinline__ uint32_t absmax(const uint32_t (&w)[8]) {
+  uint32_t m = ptx::absmax_bf16x2(w[0], w[1]);
+#pragma unroll
+  for (int i = 2; i < 8; ++i) m = ptx::absmax_bf16x2(m, w[i]);
+  return max((m << 16) & 0x7fff0000u, m & 0x7fff0000u);
 }
-__device__ __forceinline__ void put(uint32_t (&w)[8], int i, float a, float b) {
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i / 2]) : "f"(b), "f"(a));
+// Values 2 i and 2 i + 1 of the 16 as an fp32 pair, and back.
+__device__ __forceinline__ uint64_t pair(const uint32_t (&w)[16], int i) {
+  return ptx::f2_pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+}
+__device__ __forceinline__ uint64_t pair(const uint32_t (&w)[8], int i) {
+  return ptx::f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ void put(uint32_t (&w)[16], int i, uint64_t p) {
+  float a, b;
+  ptx::f2_unpack(p, a, b);
+  w[2 * i] = __float_as_uint(a);
+  w[2 * i + 1] = __float_as_uint(b);
+}
+__device__ __forceinline__ void put(uint32_t (&w)[8], int i, uint64_t p) {
+  float a, b;
+  ptx::f2_unpack(p, a, b);
+  w[i] = ptx::pack_bf16(a, b);
 }
 
 template <typename T, int D, bool WRITE>
@@ -91,10 +112,15 @@ __global__ void __launch_bounds__(kThreads) io_kernel(const IoArgs a) {
   const int lane = threadIdx.x & 31, sub = lane % LPR;
   // a row's lanes are neighbours in one warp and take the same way
   const unsigned lanes = LPR == 32 ? 0xffffffffu : ((1u << LPR) - 1u) << (lane / LPR * LPR);
-  const int64_t tasks = (int64_t)((total + RW - 1) / RW) * a.hkv;
-  const int64_t step = (int64_t)gridDim.x * (kThreads / 32);
-  for (int64_t task = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; task < tasks; task += step) {
-    const int tg = (int)(task / a.hkv), h = (int)(task - (int64_t)tg * a.hkv);
+  // the warp's tasks: RW tokens of one head each, `step` tasks apart; divided once
+  const int step = (int)gridDim.x * (kThreads / 32), step_g = step / a.hkv, step_h = step - step_g * a.hkv;
+  const int first = (int)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+  int tg = first / a.hkv, h = first - tg * a.hkv, s = 0;
+  for (; (int64_t)tg * RW < total; tg += step_g, h += step_h) {
+    if (h >= a.hkv) {
+      h -= a.hkv;
+      if ((int64_t)++tg * RW >= total) break;
+    }
     const int t = tg * RW + lane / LPR;
     if (t >= total) continue;
     const size_t row = ((size_t)t * a.hkv + h) * D + sub * 16;
@@ -103,7 +129,7 @@ __global__ void __launch_bounds__(kThreads) io_kernel(const IoArgs a) {
       load16(static_cast<const T *>(a.k) + row, x[0]);
       load16(static_cast<const T *>(a.v) + row, x[1]);
     }
-    const int s = seq_of(cu, n, t);
+    if (t < cu[s] || t >= cu[s + 1]) s = seq_of(cu, n, t);    // mostly the sequence of the task before
     const int pos = kv[s] - cu[s + 1] + t;         // kv_len - q_len + (t - cu[s])
     const int page = a.page_table[(size_t)s * a.max_pages + (pos >> a.p_shift)];
     const bool ok = page >= 0 && page < a.num_pages;
@@ -114,22 +140,22 @@ __global__ void __launch_bounds__(kThreads) io_kernel(const IoArgs a) {
     if (WRITE) {
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
-        // |x| as integers: ordered like the values, with infinities and NaN on top
-        uint32_t amax = 0;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) amax = max(amax, __float_as_uint(value(x[v], i)) & 0x7fffffffu);
+        uint32_t amax = absmax(x[v]);
 #pragma unroll
         for (int o = 1; o < LPR; o <<= 1) amax = max(amax, __shfl_xor_sync(lanes, amax, o));
         const uint32_t code = scale_code(amax);
         const float inv = code == kScaleNan ? 0.f : inverse_scale(code);
         if (!ok) continue;
+        const uint64_t inv2 = ptx::f2_pack(inv, inv);
         uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[i] = code == kScaleNan
-                     ? 0u
-                     : to_e4m3x2(value(x[v], 4 * i) * inv, value(x[v], 4 * i + 1) * inv) |
-                           (to_e4m3x2(value(x[v], 4 * i + 2) * inv, value(x[v], 4 * i + 3) * inv) << 16);
+        for (int i = 0; i < 4; ++i) {
+          float f[4];
+          ptx::f2_unpack(ptx::f2_mul(pair(x[v], 2 * i), inv2), f[0], f[1]);
+          ptx::f2_unpack(ptx::f2_mul(pair(x[v], 2 * i + 1), inv2), f[2], f[3]);
+          w[i] = to_e4m3x2(f[0], f[1]) | (to_e4m3x2(f[2], f[3]) << 16);
+        }
+        if (code == kScaleNan) w[0] = w[1] = w[2] = w[3] = 0;
         *reinterpret_cast<uint4 *>((v ? a.c.v : a.c.k) + crow) = make_uint4(w[0], w[1], w[2], w[3]);
         if (sub == 0) (v ? a.c.vs : a.c.ks)[srow] = (uint8_t)code;
       }
@@ -145,13 +171,14 @@ __global__ void __launch_bounds__(kThreads) io_kernel(const IoArgs a) {
       for (int v = 0; v < 2; ++v) {
         // a page outside the pool reads as zeros
         const float scale = ok ? scale_value(sc[v]) : 0.f;
+        const uint64_t scale2 = ptx::f2_pack(scale, scale);
         const uint32_t w[4] = {c[v].x, c[v].y, c[v].z, c[v].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float g[4];
           e4m3x4_to_f32(ok ? w[i] : 0u, g);
-          put(x[v], 4 * i, g[0] * scale, g[1] * scale);
-          put(x[v], 4 * i + 2, g[2] * scale, g[3] * scale);
+          put(x[v], 2 * i, ptx::f2_mul(ptx::f2_pack(g[0], g[1]), scale2));
+          put(x[v], 2 * i + 1, ptx::f2_mul(ptx::f2_pack(g[2], g[3]), scale2));
         }
         store16(static_cast<T *>(v ? a.v : a.k) + row, x[v]);
       }
