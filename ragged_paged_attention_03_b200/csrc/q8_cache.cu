@@ -24,6 +24,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kLenCap = 512;    // sequences whose lengths are kept in shared memory
+// Blocks of 256 threads that an SM holds: 6 with 16-bit rows (40 registers a thread), 4 with
+// fp32 ones, whose 32 values a thread take 64 registers.  The grid is no larger than that.
+template <typename T> constexpr int kBlocks = sizeof(T) == 2 ? 6 : 4;
 
 struct IoArgs {
   void *k, *v;                 // [T, Hkv, D] rows outside the cache
@@ -88,7 +91,7 @@ __device__ __forceinline__ void put(uint32_t (&w)[8], int i, uint64_t p) {
 }
 
 template <typename T, int D, bool WRITE>
-__global__ void __launch_bounds__(kThreads) io_kernel(const IoArgs a) {
+__global__ void __launch_bounds__(kThreads, kBlocks<T>) io_kernel(const IoArgs a) {
   constexpr int LPR = D / 16;         // lanes per row
   constexpr int RW = 32 / LPR;        // rows (tokens) per warp
   __shared__ int32_t s_cu[kLenCap + 1], s_kv[kLenCap];
@@ -212,10 +215,10 @@ int io_call(void *k, void *v, const rpa_q8_cache *cache, const int32_t *page_tab
   a.p_shift = log2_of(d->page_size);
   a.num_pages = d->num_pages;
   a.max_pages = d->max_pages_per_seq;
-  // enough blocks to fill 148 SMs at 8 blocks each; longer batches loop
+  // as many blocks as the 148 SMs hold at once; longer batches loop
   const int64_t per = (512 / d->head_dim) * (kThreads / 32);     // rows of a block's warps
   const int64_t rows = ((int64_t)d->total_q_tokens + 31) / 32 * 32 * d->num_kv_heads;
-  const unsigned grid = (unsigned)std::min<int64_t>((rows + per - 1) / per, 148 * 8);
+  const unsigned grid = (unsigned)std::min<int64_t>((rows + per - 1) / per, 148 * (d->dtype == RPA_F32 ? kBlocks<float> : kBlocks<__nv_bfloat16>));
 #define RPA_Q8_IO(DD)                                                                                \
   case DD:                                                                                           \
     if (d->dtype == RPA_F32) io_kernel<float, DD, WRITE><<<grid, kThreads, 0, stream>>>(a);          \
