@@ -100,7 +100,11 @@ extern "C" RPA_API int rpa_q8_attend(const void *q, const rpa_q8_cache *cache, c
   a.causal = causal ? 1 : 0;
   a.scale = scale;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
-  cudaError_t e = launch_rows(a, *dims, max_seqs, max_q_len, w.q_limit, ws + w.rows, stream);
-  if (e == cudaSuccess && w.chunk) e = launch_chunk(a, *dims, max_seqs, max_q_len, w.q_limit, ws + w.parts, stream);
+  cudaError_t e = cudaSuccess;
+  for (const bool join : {false, true}) {
+    if (e == cudaSuccess) e = launch_rows(a, *dims, max_seqs, max_q_len, w.q_limit, ws + w.rows, join, stream);
+    if (e == cudaSuccess && w.chunk)
+      e = launch_chunk(a, *dims, max_seqs, max_q_len, w.q_limit, ws + w.parts, join, stream);
+  }
   return e == cudaSuccess ? RPA_OK : RPA_ERR_CUDA;
 }

@@ -1058,7 +1058,8 @@ __global__ void __launch_bounds__(256) combine_kernel(const Args g) {
 }
 
 template <int D>
-cudaError_t launch_t(const AttendArgs &a, int q_limit, int total_q, int grid, uint8_t *ws, cudaStream_t stream) {
+cudaError_t launch_t(const AttendArgs &a, int q_limit, int total_q, int grid, uint8_t *ws, bool join,
+                     cudaStream_t stream) {
   using S = Shape<D>;
   Args g{};
   g.a = a;
@@ -1069,6 +1070,10 @@ cudaError_t launch_t(const AttendArgs &a, int q_limit, int total_q, int grid, ui
   g.heads = reinterpret_cast<PartHead *>(ws + w.heads);
   g.ml = reinterpret_cast<float2 *>(ws + w.ml);
   g.o = reinterpret_cast<float4 *>(ws + w.o);
+  if (join) {
+    if (grid == 1) return cudaSuccess;
+    return launch_behind(combine_kernel<D>, S::ROWS / 16 * grid, 256, 0, stream, g);
+  }
   CUtensorMap tk, tv;
   const uint64_t cdims[3] = {(uint64_t)D, (uint64_t)a.hkv, (uint64_t)a.num_pages * a.p};
   const uint64_t cstrides[2] = {(uint64_t)D, (uint64_t)a.hkv * D};
@@ -1085,9 +1090,7 @@ cudaError_t launch_t(const AttendArgs &a, int q_limit, int total_q, int grid, ui
   auto kern = chunk_kernel<D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
-  e = launch_behind(kern, grid, kThreads, S::kSmem, stream, tq, tk, tv, g);
-  if (e != cudaSuccess || grid == 1) return e;
-  return launch_behind(combine_kernel<D>, S::ROWS / 16 * grid, 256, 0, stream, g);
+  return launch_behind(kern, grid, kThreads, S::kSmem, stream, tq, tk, tv, g);
 }
 
 }  // namespace
@@ -1118,12 +1121,12 @@ ChunkLayout chunk_layout(int grid, int D) {
 }
 
 cudaError_t launch_chunk(const AttendArgs &a, const rpa_dims &d, int32_t max_seqs, int32_t max_q, int32_t q_limit,
-                         uint8_t *ws, cudaStream_t stream) {
+                         uint8_t *ws, bool join, cudaStream_t stream) {
   const int grid = chunk_grid(d, max_seqs, max_q);
   switch (d.head_dim) {
-    case 64: return launch_t<64>(a, q_limit, d.total_q_tokens, grid, ws, stream);
-    case 128: return launch_t<128>(a, q_limit, d.total_q_tokens, grid, ws, stream);
-    case 256: return launch_t<256>(a, q_limit, d.total_q_tokens, grid, ws, stream);
+    case 64: return launch_t<64>(a, q_limit, d.total_q_tokens, grid, ws, join, stream);
+    case 128: return launch_t<128>(a, q_limit, d.total_q_tokens, grid, ws, join, stream);
+    case 256: return launch_t<256>(a, q_limit, d.total_q_tokens, grid, ws, join, stream);
     default: return cudaErrorInvalidValue;
   }
 }

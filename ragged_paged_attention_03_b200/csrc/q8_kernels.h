@@ -43,7 +43,10 @@ cudaError_t launch_behind(K kern, int grid, int threads, int smem, cudaStream_t 
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-// Few query rows per KV head.  Sequences with q_len > q_limit are left out.
+// Few query rows per KV head.  Sequences with q_len > q_limit are left out.  launch_rows is called
+// twice: without `join` for the attention itself, and with it, behind the chunk kernel where the
+// call has one, for joining the parts that several CTAs share (between the two attention
+// kernels it would keep the second from beginning as the first ends).
 int rows_per_group(const rpa_dims &d, int32_t max_q);
 int rows_grid(const rpa_dims &d, int32_t max_seqs, int32_t max_q, int R);
 struct RowsLayout {
@@ -51,7 +54,7 @@ struct RowsLayout {
 };
 RowsLayout rows_layout(int grid, int R, int D);
 cudaError_t launch_rows(const AttendArgs &a, const rpa_dims &d, int32_t max_seqs, int32_t max_q, int32_t q_limit,
-                        uint8_t *ws, cudaStream_t stream);
+                        uint8_t *ws, bool join, cudaStream_t stream);
 
 // Chunks of query rows (bf16).  Sequences with q_len <=
 // q_limit are left out.
@@ -61,9 +64,10 @@ struct ChunkLayout {
   int64_t heads, ml, o, total;
 };
 ChunkLayout chunk_layout(int grid, int D);
-// It is queued with launch_behind, right behind the row-group kernels of the call.
+// Called twice as launch_rows; the first, the attention, is queued with launch_behind
+// right behind the row-group kernel of the call.
 cudaError_t launch_chunk(const AttendArgs &a, const rpa_dims &d, int32_t max_seqs, int32_t max_q, int32_t q_limit,
-                         uint8_t *ws, cudaStream_t stream);
+                         uint8_t *ws, bool join, cudaStream_t stream);
 
 }  // namespace q8
 }  // namespace rpa

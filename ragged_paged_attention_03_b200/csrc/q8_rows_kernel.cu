@@ -34,7 +34,7 @@
 // heads with the same run are neighbours: they read the rows of a token, which lie
 // side by side, at about the same time.  A run may begin and
 // end inside a group: those partial results go to the workspace and
-// combine_kernel, queued behind with programmatic dependent launch, joins them
+// combine_kernel, queued with programmatic dependent launch, joins them
 // in the order of the keys (the same bits every time).
 //
 // Warps: 0-3 the parts of Q (a row each at a time; one warp for all of them took
@@ -855,14 +855,8 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const Args g) {
 }
 
 template <typename T, int D, int R>
-cudaError_t launch_t(const AttendArgs &a, int q_limit, int grid, uint8_t *ws, cudaStream_t stream) {
+cudaError_t launch_t(const AttendArgs &a, int q_limit, int grid, uint8_t *ws, bool join, cudaStream_t stream) {
   using S = Shape<T, D, R>;
-  CUtensorMap tk, tv;
-  const uint64_t dims[3] = {(uint64_t)D, (uint64_t)a.hkv, (uint64_t)a.num_pages * a.p};
-  const uint64_t strides[2] = {(uint64_t)D, (uint64_t)a.hkv * D};
-  const uint32_t box[3] = {(uint32_t)S::W, 1, (uint32_t)(a.p < BN ? a.p : BN)};
-  if (!make_tmap_u8_3d(&tk, a.c.k, dims, strides, box, true) || !make_tmap_u8_3d(&tv, a.c.v, dims, strides, box, true))
-    return cudaErrorInvalidValue;
   Args g{};
   g.a = a;
   g.q_limit = q_limit;
@@ -870,13 +864,21 @@ cudaError_t launch_t(const AttendArgs &a, int q_limit, int grid, uint8_t *ws, cu
   g.heads = reinterpret_cast<PartHead *>(ws + w.heads);
   g.ml = reinterpret_cast<float *>(ws + w.ml);
   g.o = reinterpret_cast<float *>(ws + w.o);
+  if (join) {
+    if (grid == a.hkv) return cudaSuccess;   // one run per head: nothing is split
+    return launch_behind(combine_kernel<T, D, R>, grid, kJoinThreads, 0, stream, g);
+  }
+  CUtensorMap tk, tv;
+  const uint64_t dims[3] = {(uint64_t)D, (uint64_t)a.hkv, (uint64_t)a.num_pages * a.p};
+  const uint64_t strides[2] = {(uint64_t)D, (uint64_t)a.hkv * D};
+  const uint32_t box[3] = {(uint32_t)S::W, 1, (uint32_t)(a.p < BN ? a.p : BN)};
+  if (!make_tmap_u8_3d(&tk, a.c.k, dims, strides, box, true) || !make_tmap_u8_3d(&tv, a.c.v, dims, strides, box, true))
+    return cudaErrorInvalidValue;
   auto kern = rows_kernel<T, D, R>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
   kern<<<grid, kThreads, S::kSmem, stream>>>(tk, tv, g);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || grid == a.hkv) return e;   // one run per head: nothing is split
-  return launch_behind(combine_kernel<T, D, R>, grid, kJoinThreads, 0, stream, g);
+  return cudaGetLastError();
 }
 
 template <typename T, int D, int R> constexpr int ctas_of() { return Shape<T, D, R>::CTAS; }
@@ -929,17 +931,17 @@ RowsLayout rows_layout(int grid, int R, int D) {
 }
 
 cudaError_t launch_rows(const AttendArgs &a, const rpa_dims &d, int32_t max_seqs, int32_t max_q, int32_t q_limit,
-                        uint8_t *ws, cudaStream_t stream) {
+                        uint8_t *ws, bool join, cudaStream_t stream) {
   const int R = rows_per_group(d, std::min(max_q, q_limit));
   const int grid = rows_grid(d, max_seqs, std::min(max_q, q_limit), R);
 #define RPA_Q8_ROWS(DD)                                                                                   \
   case DD:                                                                                                \
     if (d.dtype == RPA_F32)                                                                               \
-      return R == 4 ? launch_t<float, DD, 4>(a, q_limit, grid, ws, stream)                                \
-                    : launch_t<float, DD, 8>(a, q_limit, grid, ws, stream);                               \
-    return R == 4   ? launch_t<__nv_bfloat16, DD, 4>(a, q_limit, grid, ws, stream)                        \
-           : R == 8 ? launch_t<__nv_bfloat16, DD, 8>(a, q_limit, grid, ws, stream)                        \
-                    : launch_t<__nv_bfloat16, DD, 16>(a, q_limit, grid, ws, stream);
+      return R == 4 ? launch_t<float, DD, 4>(a, q_limit, grid, ws, join, stream)                                \
+                    : launch_t<float, DD, 8>(a, q_limit, grid, ws, join, stream);                               \
+    return R == 4   ? launch_t<__nv_bfloat16, DD, 4>(a, q_limit, grid, ws, join, stream)                        \
+           : R == 8 ? launch_t<__nv_bfloat16, DD, 8>(a, q_limit, grid, ws, join, stream)                        \
+                    : launch_t<__nv_bfloat16, DD, 16>(a, q_limit, grid, ws, join, stream);
   switch (d.head_dim) {
     RPA_Q8_ROWS(64)
     RPA_Q8_ROWS(128)
