@@ -127,27 +127,6 @@ struct Args {
   float4 *o;             // [2 * ctas][D / 4][ROWS]
 };
 
-// Waits for a phase, for at most kWaitLimitNs: false, with RPA_DEV_TIMEOUT raised,
-// when that runs out or another warp gave up.  The clock is looked at every 64 polls.
-__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort_flag, uint32_t *err) {
-  uint32_t n = 0;
-  uint64_t t0 = 0;
-  while (!ptx::mbar_try_wait(bar, parity)) {
-    if ((++n & 63) != 0) continue;
-    const uint64_t now = ptx::globaltimer();
-    if (n == 64) t0 = now;
-    if (*abort_flag || now - t0 > ptx::kWaitLimitNs) {
-      *abort_flag = 1;
-      raise(err, RPA_DEV_TIMEOUT);
-      return false;
-    }
-  }
-  return true;
-}
-__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort_flag, uint32_t *err) {
-  return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, err));
-}
-
 // sum over i in [0, n) of floor((a i + b) / M), a, b >= 0: by the quotients and
 // remainders of a and b, which leaves floor((a' i + b') / M) with a', b' < M; its sum
 // repeats every M terms.
@@ -638,28 +617,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int v = 0; v < 2; ++v) {
           const int use = 2 * gb + v, cs = use % S::NST;
-          uint32_t fac[NU / 2];
-          {
-            const uint16_t *fp = s_fac + (gb & 1) * 2 * BN + v * BN + row0;
-            if constexpr (NU == 8) {
-              const uint4 q = *reinterpret_cast<const uint4 *>(fp);
-              fac[0] = q.x; fac[1] = q.y; fac[2] = q.z; fac[3] = q.w;
-            } else {
-              const uint2 q = *reinterpret_cast<const uint2 *>(fp);
-              fac[0] = q.x; fac[1] = q.y;
-            }
-          }
+          const uint16_t *fac = s_fac + (gb & 1) * 2 * BN + v * BN + row0;
           ok = gb < NSK || wait_warp(v ? &bars->v_empty[st] : &bars->k_empty[st], (uint32_t)(((gb / NSK) & 1) ^ 1),
                                      abort_flag, err);
           ok = ok && wait_warp(&bars->c_full[cs], (uint32_t)((use / S::NST) & 1), abort_flag, err);
           if (!ok) break;
           const uint8_t *src = sC + cs * S::kCodes + src0;
           uint8_t *dst = (v ? sV : sK) + st * S::kKVBytes + dst0;
-#pragma unroll
+          // two rows at a time: eight were 8 KB of code, which the caches did not hold beside the
+          // softmax's (8 prompts of 2048 tokens 475 us, with two 444)
+#pragma unroll 2
           for (int i = 0; i < NU; ++i) {
             uint2 a0 = *reinterpret_cast<const uint2 *>(src + i * D);
             uint2 a1 = *reinterpret_cast<const uint2 *>(src + i * D + (swp ? -8 : 8));
-            const uint32_t f = __byte_perm(fac[i / 2], 0u, i & 1 ? 0x3232 : 0x1010);
+            const uint32_t f = __byte_perm((uint32_t)fac[i], 0u, 0x1010);
             *reinterpret_cast<uint4 *>(dst + i * 128 + ((x0 ^ i) << 4)) =
                 make_uint4(mul_h2(codes_h2(a0.x), f), mul_h2(codes_h2(a0.x >> 16), f),
                            mul_h2(codes_h2(a0.y), f), mul_h2(codes_h2(a0.y >> 16), f));

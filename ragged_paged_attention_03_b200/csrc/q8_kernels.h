@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "ptx.cuh"
 #include "q8_common.cuh"
 #include "rpa.h"
 
@@ -24,6 +25,30 @@ struct AttendArgs {
 
 __device__ __forceinline__ void store(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+// Waits for a phase, for at most kWaitLimitNs: false, with RPA_DEV_TIMEOUT raised, when
+// that runs out or another warp of the block gave up.  The clock is looked at every 64
+// polls.  The poll loop is a function of its own, not part of every wait: these kernels'
+// warps run long straight loops that share the instruction caches, and with it inlined the
+// chunk kernel took 444 us for 8 prompts of 2048 tokens instead of 414.
+inline __device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity, volatile int *abort_flag, uint32_t *err) {
+  const uint64_t t0 = ptx::globaltimer();
+  for (uint32_t n = 1; !ptx::mbar_try_wait(bar, parity); ++n) {
+    if ((n & 63) != 0) continue;
+    if (*abort_flag || ptx::globaltimer() - t0 > ptx::kWaitLimitNs) {
+      *abort_flag = 1;
+      raise(err, RPA_DEV_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort_flag, uint32_t *err) {
+  return ptx::mbar_try_wait(bar, parity) || wait_long(bar, parity, abort_flag, err);
+}
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort_flag, uint32_t *err) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, err));
+}
 
 // A launch that may begin while the kernel queued before it on `stream` ends
 // (programmatic dependent launch).  Every kernel of these files waits for what it

@@ -122,23 +122,6 @@ struct Args {
   float *o;                      // [2 * ctas][R][D] unnormalised
 };
 
-__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort_flag, uint32_t *err) {
-  if (ptx::mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = ptx::globaltimer();
-  while (!ptx::mbar_try_wait(bar, parity)) {
-    if (*abort_flag) return false;
-    if (ptx::globaltimer() - t0 > ptx::kWaitLimitNs) {
-      *abort_flag = 1;
-      raise(err, RPA_DEV_TIMEOUT);
-      return false;
-    }
-  }
-  return true;
-}
-__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort_flag, uint32_t *err) {
-  return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, err));
-}
-
 // Blocks of one sequence: groups of R rows per KV head, each of nb blocks (a
 // sequence without keys has one, empty, so that its rows are written).  In the list
 // that is cut into runs a group counts kGroupCost blocks more, at its front: making Q's
