@@ -523,9 +523,11 @@ RPA_API int rpa_q8_workspace_size(const rpa_dims *dims, int32_t max_seqs,
  *   q_len: with causal == 0 this is cross attention to cached states of
  *   another length.  A row that sees no key gets out = 0 and lse = -inf.  A
  *   row that sees a token whose K or V row stands for NaN gets NaN in out and
- *   lse; a token outside a row's mask never reaches it.
+ *   lse; a token outside a row's mask never reaches it.  An infinity or a NaN in
+ *   a query row gives NaN in that row.
  * max_q_len: no q_len of the batch is above it (else RPA_DEV_BAD_LENGTHS).
- *   With max_q_len == 1 only the single-token kernel is launched.
+ *   Up to max_q_len * G <= 16 (single tokens and a few more), and for fp32
+ *   always, only the kernel of few query rows is launched.
  * workspace: caller-owned device memory, 256-byte aligned, of at least
  *   rpa_q8_workspace_size bytes, else RPA_ERR_WORKSPACE.  Its contents need no
  *   initialisation and mean nothing after the call; calls that share one must
