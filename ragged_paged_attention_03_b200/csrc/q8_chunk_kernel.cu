@@ -33,6 +33,12 @@
 // Roles (512 threads of at most 128 registers).  Every hot loop is short and
 // rolled: with five kinds of warps on an SM the unrolled forms (a row's 128 scores in
 // registers) were bound by instruction fetch, at a third of this speed.
+// Measured (Hq 32, Hkv 8, D 128): 8 prompts of 2048 tokens 407 us (676 TFLOP/s of the causal
+// products), 4 chunks of 512 behind contexts of some thousands 195 us (725 TFLOP/s).  A block of
+// 128 keys takes 4,200 to 4,900 clocks where its MMAs need 2,048: the conversion of its K and V takes
+// the converters 4,200 (1,250 each, the rest waits that are over when they are looked at), a
+// softmax step 2,000 to 2,500 of which the exponentials are 650 to 1,200, by whether both
+// tiles' are at theirs; the tensor pipe is active 36 % of the time, the issue slots 52 %.
 //   warps 0-3, 4-7  softmax and output of tile 0 and 1 (one row per thread); they
 //                   also turn their tile's Q, landed by TMA as bf16, into scaled
 //                   fp16 in place

