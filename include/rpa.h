@@ -448,7 +448,7 @@ RPA_API int rpa_host_groups(const int32_t *cu_q_lens, int32_t num_seqs,
  *
  * The lengths stay in device memory, as in rpa_forward_device: cu_q_lens
  * [max_seqs + 1], kv_lens [max_seqs] and num_seqs [1] are device int32 arrays
- * read when the kernels run (entries past num_seqs are not read), page_table
+ * read when the kernels run (entries past num_seqs may hold anything), page_table
  * is a device array of max_seqs rows, dims->total_q_tokens is the capacity T of
  * the token arrays (cu_q_lens[num_seqs] <= T), and rows from
  * cu_q_lens[num_seqs] on are neither read nor written.  What is launched

@@ -10,9 +10,9 @@
 // that their scales, single bytes, share a sector, and neighbouring warps take the
 // heads, so that together they read what lies together.
 //
-// Measured, launch included: 16,384 tokens of 8 heads, D 128, bf16, written in 20.7 us
-// (4.9 TB/s, 0.74 of a plain copy's rate) and a context of about that size read in 20.4 us;
-// below a few thousand rows a call costs its launch (3.7 us in a graph).  The write issues in
+// Measured, launch included: 16,384 tokens of 8 heads, D 128, bf16, written in 20.5 us
+// (4.9 TB/s, 0.75 of a plain copy's rate) and a context of about that size read in 19.6 us;
+// below a few thousand rows a call costs its launch (3.0 us in a graph).  The write issues in
 // 61 % of its slots: maxima, products and conversions, not the memory, set the rest.
 #include <algorithm>
 #include <cuda_runtime.h>
@@ -100,22 +100,50 @@ __global__ void __launch_bounds__(kThreads, kBlocks<T>) io_kernel(const IoArgs a
   constexpr int LPR = D / 16;         // lanes per row
   constexpr int RW = 32 / LPR;        // rows (tokens) per warp
   __shared__ int32_t s_cu[kLenCap + 1], s_kv[kLenCap];
-  const int n = checked_seqs(a.len);
+  // The lengths, checked, and in shared memory where they fit.  Where the arrays fit, in one pass
+  // that reads them beside the count (entries past it lie within the arrays and are dropped):
+  // one latency instead of three.
+  const int32_t *cu = a.len.cu, *kv = a.len.kv;
+  int n;
+  if (a.len.max_seqs <= kLenCap) {
+    constexpr int PER = kLenCap / kThreads;
+    int c0[PER], c1[PER], k[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int i = threadIdx.x + j * kThreads;
+      if (i < a.len.max_seqs) c0[j] = cu[i], c1[j] = cu[i + 1], k[j] = kv[i];
+    }
+    n = *a.len.num_seqs;
+    int bad = n < 0 || n > a.len.max_seqs;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int i = threadIdx.x + j * kThreads;
+      if (bad || i >= n) continue;
+      bad |= breaks(a.len, n, i, c0[j], c1[j], k[j]);
+      s_cu[i] = c0[j];
+      s_kv[i] = k[j];
+      if (i == n - 1) s_cu[n] = c1[j];
+    }
+    if (__syncthreads_or(bad)) n = -1;
+    cu = s_cu;
+    kv = s_kv;
+  } else {
+    n = checked_seqs(a.len);
+    if (n >= 0 && n <= kLenCap) {
+      for (int i = threadIdx.x; i <= n; i += kThreads) {
+        s_cu[i] = cu[i];
+        if (i < n) s_kv[i] = kv[i];
+      }
+      __syncthreads();
+      cu = s_cu;
+      kv = s_kv;
+    }
+  }
   if (n < 0) {
     if (blockIdx.x == 0 && threadIdx.x == 0) raise(a.err, RPA_DEV_BAD_LENGTHS);
     return;
   }
   if (n == 0) return;
-  const int32_t *cu = a.len.cu, *kv = a.len.kv;
-  if (n <= kLenCap) {
-    for (int i = threadIdx.x; i <= n; i += kThreads) {
-      s_cu[i] = a.len.cu[i];
-      if (i < n) s_kv[i] = a.len.kv[i];
-    }
-    __syncthreads();
-    cu = s_cu;
-    kv = s_kv;
-  }
   const int total = cu[n];
   const int lane = threadIdx.x & 31, sub = lane % LPR;
   // a row's lanes are neighbours in one warp and take the same way

@@ -44,6 +44,13 @@ __device__ __forceinline__ void raise(uint32_t *err, uint32_t bits) {
   if (err != nullptr) atomicOr(err, bits);
 }
 
+// 1 if sequence s of n, whose tokens are x0 .. x1 - 1, breaks a rule.
+__device__ __forceinline__ int breaks(const Lengths &a, int n, int s, int x0, int x1, int kv) {
+  const int64_t ql = (int64_t)x1 - x0;
+  return ql < 0 || kv < 0 || kv > a.cap || (a.max_q >= 0 && ql > a.max_q) || (a.self && kv < ql) ||
+         (s == 0 && x0 != 0) || (s == n - 1 && x1 > a.T);
+}
+
 // Checks the lengths by every thread of the block (a read of the whole list:
 // kernels that run many blocks share it through L2).  Returns the number of
 // sequences, or -1 (uniform in the block) when a rule is broken.  Contains
@@ -52,12 +59,7 @@ __device__ __forceinline__ int checked_seqs(const Lengths &a) {
   const int n = *a.num_seqs;
   int bad = n < 0 || n > a.max_seqs;
   if (!bad) {
-    if (threadIdx.x == 0) bad = a.cu[0] != 0 || a.cu[n] > a.T;
-    for (int s = threadIdx.x; s < n; s += blockDim.x) {
-      const int64_t ql = (int64_t)a.cu[s + 1] - a.cu[s];
-      const int kv = a.kv[s];
-      bad |= ql < 0 || kv < 0 || kv > a.cap || (a.max_q >= 0 && ql > a.max_q) || (a.self && kv < ql);
-    }
+    for (int s = threadIdx.x; s < n; s += blockDim.x) bad |= breaks(a, n, s, a.cu[s], a.cu[s + 1], a.kv[s]);
   }
   return __syncthreads_or(bad) ? -1 : n;
 }
@@ -87,11 +89,7 @@ __device__ __forceinline__ Start find_start(const Lengths &a, int cta, int ctas,
   }
   const int n = *a.num_seqs;
   int bad = n < 0 || n > a.max_seqs;
-  auto check = [&](int s, int x0, int x1, int k) {
-    const int64_t ql = (int64_t)x1 - x0;
-    bad |= ql < 0 || k < 0 || k > a.cap || (a.max_q >= 0 && ql > a.max_q) || (a.self && k < ql) ||
-           (s == 0 && x0 != 0) || (s == n - 1 && x1 > a.T);
-  };
+  auto check = [&](int s, int x0, int x1, int k) { bad |= breaks(a, n, s, x0, x1, k); };
   auto warp_scan = [&](int64_t v) -> int64_t {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {

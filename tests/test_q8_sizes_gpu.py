@@ -20,10 +20,10 @@ def many(n, dtype, seed, d=64, hq=4, hkv=2, p=8):
 
 # 224, 256, 512 threads validate and scan the lengths; 512 fit in shared memory
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("n", [225, 257, 513, 1100])
-def test_many_sequences(n, dtype):
+@pytest.mark.parametrize("n,more", [(225, 3), (257, 3), (513, 3), (1100, 3), (30, 900), (512, 0), (509, 3), (510, 3)])
+def test_many_sequences(n, more, dtype):
     pr = many(n, dtype, n)
-    dv = Dev(pr, more_seqs=3, more_rows=2)
+    dv = Dev(pr, more_seqs=more, more_rows=2)
     dv.attend().checked(what=f"{n} sequences")
     t = sum(pr.q_lens)
     rows = [new_rows(pr, 7 + i, dtype, odd=False) for i in range(2)]
