@@ -656,6 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::mbar_arrive(v ? &bars->v_full[st] : &bars->k_full[st]);
           ptx::mbar_arrive(&bars->c_empty[cs]);
         }
+        __syncwarp();                     // the other lanes have read their factors too
         if (lane == 0) ptx::mbar_arrive(&bars->f_empty[gb & 1]);
       }
     }
