@@ -17,13 +17,13 @@ def places(pr, s, pos):
 
 @pytest.mark.parametrize("d", [64, 128, 256])
 def test_chunk_scales_change_from_block_to_block(d):
-    """V scales that swing by 2^14 from each 64 keys to the next: a factor taken
-    from another block's slot would show at once.  Repeats bit for bit."""
+    """V scales that differ by 2^6 from key to key, the other way round in the next
+    block: a factor taken from another block would show at once.  Repeats bit for bit."""
     pr = R.make([300, 150, 280], [3000, 2500, 280], hq=4, hkv=4, d=d, p=16, seed=3)
     for s, b in enumerate(pr.kv_lens):
         pos = torch.arange(b)
         page, slot = places(pr, s, pos)
-        up = (pos // 64 % 2 * 14).to(torch.uint8)[:, None]
+        up = ((pos + pos // 128) % 2 * 6).to(torch.uint8)[:, None]
         pr.v_scales[page, :, slot] += up
     dv = Dev(pr).attend()
     dv.checked(what=f"head_dim {d}")
