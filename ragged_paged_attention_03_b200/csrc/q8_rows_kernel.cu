@@ -315,6 +315,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
     const int nseg = BN / br;
     const uint32_t seg_bytes = (uint32_t)(br * D);
     int gb = 0;
+    int queued[2] = {0, 0};                // K and V tiles: a wait that gives up may leave them unequal
     bool ok = true;
     while (ok && run.next()) {
       const int last = run.last_block();
@@ -353,16 +354,17 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
             for (int c = 0; c < S::CT; ++c)
               ptx::tma_load_3d_hint(dst + c * BN * S::W, kv ? &tm_v : &tm_k, full, c * S::W, run.hk, row, once);
           __syncwarp();
+          ++queued[kv];
         }
         if (!ok) break;
       }
     }
     // every queued copy lands before the CTA ends
     if (lane == 0)
-      for (int k = gb - NS < 0 ? 0 : gb - NS; k < gb; ++k) {
-        ptx::mbar_wait(&bars->k_full[k % NS], (uint32_t)((k / NS) & 1));
-        ptx::mbar_wait(&bars->v_full[k % NS], (uint32_t)((k / NS) & 1));
-      }
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv)
+        for (int k = max(0, queued[kv] - NS); k < queued[kv]; ++k)
+          ptx::mbar_wait(kv ? &bars->v_full[k % NS] : &bars->k_full[k % NS], (uint32_t)((k / NS) & 1));
     __syncwarp();
   } else if (warp == 5) {
     // ------------------------------------------------------------ MMA
