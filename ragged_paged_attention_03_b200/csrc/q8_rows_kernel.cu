@@ -638,12 +638,14 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
 #pragma unroll
           for (int r = 0; r < R; ++r) {
             const float mb = fmaxf(fmaxf(wm[r], wm[32 + r]), fmaxf(wm[64 + r], wm[96 + r]));
-            const float yb = joined(fmaxf(fmaxf(wm[16 + r], wm[48 + r]), fmaxf(wm[80 + r], wm[112 + r])));
+            // -inf where the row sees nothing of the block: its weights are zeros then, and so is
+            // what they count (joined(yb) in its place would be 2^-m, which overflows for low scores)
+            const float yb = fmaxf(fmaxf(wm[16 + r], wm[48 + r]), fmaxf(wm[80 + r], wm[112 + r]));
             const float mn = fmaxf(m[r], mb);
             al[r] = m[r] == mn ? 1.f : ptx::ex2(m[r] - mn);
             m[r] = mn;
             l[r] = l[r] * al[r] + ptx::ex2(x[r] - joined(mn));
-            w[r] = ptx::ex2((x[r] + (8.f - yb)) + ev);
+            w[r] = ptx::ex2((x[r] + (8.f - joined(yb))) + ev);
             Fn[r] = ptx::ex2(yb - joined(mn) - 8.f);
           }
           uint32_t pw[S::CP / 4];
