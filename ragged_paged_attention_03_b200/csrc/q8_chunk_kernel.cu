@@ -746,7 +746,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int ek = 0, ev = 0;
       bool wide_k = false, wide_v = false;
       float m = -INFINITY, l = 0.f;                   // l counts 2^kBase per unit weight
-      int evr = 0;                                    // O is in units of 2^(m + evr - kBase)
+      float evf = 0.f;                                // log2 of the row's largest contribution so far, less m,
+      int evr = 0;                                    // rounded up: O is in units of 2^(m + evr - kBase)
       for (int j = 0; j < nt; ++j) {                  // steps
         const int blk = gb + j / SPB, eslot = blk % kExpSlots, buf = (gt + j) & 1;
         const uint32_t tS = lane_base + (uint32_t)(t * 128 + buf * HN);
@@ -797,10 +798,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (j > 0 && !wait_warp(&bars->pv_done[t][buf ^ 1], (uint32_t)(((gt + j - 1) >> 1) & 1), abort_flag, err))
               return false;
             ptx::tc_fence_after();
-            // The new units: the larger of the old ones and the block's largest contribution
-            // (a row that has seen nothing has no old ones)
-            const float top = m == -INFINITY ? my + (float)ev : fmaxf(m + (float)evr, my + (float)ev);
-            const int evn = m_new == -INFINITY || top == -INFINITY ? evr : (int)ceilf(fmaxf(top - m_new, -300.f));
+            // The new units: the larger of the old ones and the block's largest contribution (a row
+            // that has seen nothing has no old ones), relative to 2^m and with their fraction: whole
+            // octaves taken from the whole ones of the time before would gain up to one each time, and
+            // every row of the warp comes by whenever one of them needs it
+            const float was = m == -INFINITY ? -INFINITY : evf + (m - m_new);
+            if (m_new != -INFINITY) evf = fmaxf(fmaxf(was, (my - m_new) + (float)ev), -300.f);
+            const int evn = (int)ceilf(evf);
             const float am = m == -INFINITY ? 0.f : ptx::ex2(m - m_new);
             const float alpha = m == -INFINITY ? 0.f : ptx::ex2((m - m_new) + (float)(evr - evn));
             if (j > 0) {

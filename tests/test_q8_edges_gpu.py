@@ -1,6 +1,8 @@
 """The 8-bit cache's kernels where their bookkeeping or arithmetic can go wrong:
 rings, masks that leave a block's rows empty, units of the accumulators, rows
 of zeros, the top of the format's range."""
+from dataclasses import replace
+
 import pytest
 import torch
 
@@ -56,3 +58,46 @@ def test_rows_without_a_key_in_a_block_and_low_scores(dtype, hq, q_len, by):
                 dtype=dtype, seed=5)
     low_scores(pr, by)
     Dev(pr).attend().checked(what=f"scores around -{by}")
+
+
+def set_rows(pr, s, k, v):
+    """Sequence s holds the rows k, v [kv_len, Hkv, D], quantised."""
+    page, slot = places(pr, s, torch.arange(pr.kv_lens[s]))
+    for x, codes, scales in ((k, pr.k_codes, pr.k_scales), (v, pr.v_codes, pr.v_scales)):
+        c, e = R.quantise_row(x)
+        codes[page, slot] = c
+        scales[page, :, slot] = e
+
+
+@pytest.mark.parametrize("fade", [0.0, 0.35])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_rows_beside_one_whose_maximum_climbs(d, fade):
+    """One row's scores climb by 10 every 64 keys, which rescales its warp's sums each time.  The
+    other rows have flat scores, of maxima from 90 to 180, or scores that climb slowly on values
+    that shrink by 2^fade every 64 keys: their outputs count every key.  The sequence many times
+    over, so that one CTA runs over most of it."""
+    steps, gen = 60, torch.Generator().manual_seed(7)
+    n = 64 * steps
+    pr = R.make([64], [n], hq=1, hkv=1, d=d, p=16, causal=False, scale=0.7)
+    t = 14 * (torch.arange(n) // 64)
+    k = torch.zeros(n, 1, d)
+    for i, cap in enumerate((448, 448, 16)):           # exact codes: multiples of 32, then small integers
+        part = (t - t % 32 if i < 2 else t).clamp(max=cap)
+        k[:, 0, i] = part
+        t = t - part
+    k[:, 0, 3] = t
+    k[:, 0, 5] = 128.0
+    k[:, 0, 6] = fade * torch.log(torch.tensor(2.0)) / 0.7 * (torch.arange(n) // 64) * 32
+    v = torch.rand(n, 1, d, generator=gen) + 0.5
+    v *= torch.exp2(-fade * (torch.arange(n) // 64))[:, None, None]
+    set_rows(pr, 0, k, v)
+    pr.q[:] = 0
+    pr.q[:, 0, 5] = 1 + torch.arange(64) / 64
+    pr.q[:, 0, 6] = 1 / 32
+    for r in (5, 37):                                  # one row of each warp
+        pr.q[r] = 0
+        pr.q[r, 0, :4] = 1
+    ref, times = R.attend(pr), 150
+    pr = replace(pr, q_lens=pr.q_lens * times, kv_lens=pr.kv_lens * times, table=pr.table.repeat(times, 1),
+                 q=pr.q.repeat(times, 1, 1))
+    Dev(pr).attend().checked([x.repeat(times, *[1] * (x.dim() - 1)) for x in ref], what=f"head_dim {d}")
