@@ -600,7 +600,25 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, D, R>::CTAS))
           ptx::mbar_arrive(&bars->sc_empty[slot]);
           // NaN of either scale makes the score NaN for the rows that see the key
           const float kf = scale_value(kc) + (vc == kScaleNan ? NAN : 0.f);
-          const float ev = key && vc != kScaleNan ? (float)((int)vc - 127) : 0.f;
+          // A V row of zeros adds nothing, so its scale must not set the unit of the block's weights
+          // (a key of most of the weight, whose row is zeros, would leave the others no bits).  The
+          // format gives such rows the scale 2^0, or the smallest one: only those are looked through.
+          bool zero = key && (vc == kScaleOne || vc == 0);
+          if (__any_sync(0xffffffffu, zero)) {
+            const int st = gb % NS;
+            if (!wait_warp(&bars->v_full[st], (uint32_t)((gb / NS) & 1), abort_flag, a.err)) {
+              ok = false;
+              break;
+            }
+            const uint8_t *row = sV + st * S::kTile + tid * S::W;
+#pragma unroll 1
+            for (int q = 0; zero && q < D / 16; ++q) {
+              const int c = q * 16 / S::W, i = (q + tid) % (S::W / 16);   // lanes start at different banks
+              const uint4 v = *reinterpret_cast<const uint4 *>(row + c * BN * S::W + i * 16);
+              zero = ((v.x | v.y | v.z | v.w) & 0x7f7f7f7fu) == 0;
+            }
+          }
+          const float ev = zero ? -INFINITY : key && vc != kScaleNan ? (float)((int)vc - 127) : 0.f;
           if (!wait_warp(&bars->s_full[par], (uint32_t)((gb >> 1) & 1), abort_flag, a.err)) {
             ok = false;
             break;
