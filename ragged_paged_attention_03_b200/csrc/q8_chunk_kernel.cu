@@ -72,7 +72,10 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 6.0f;    // lazy rescale of O: weights reach 2^(6 + kBase)
 constexpr int kBase = 5;
 constexpr int kWide = 15;           // a tile whose scales spread further is "wide"
+constexpr int kLift = 100;          // weights whose V rows are zeros pass the units of O by 2^kLift at most
 constexpr int kWideBit = 1 << 16;   // in the published ekb / evb
+constexpr int kZeroBit = 1 << 17;   // in the published evb: the tile has V rows of zeros
+constexpr int kExpWords = 6;        // published of a block: ekb, evb, V rows of zeros (word k: keys 4 i + k)
 constexpr int kExpSlots = 8;
 constexpr int kSegSlots = 4;
 
@@ -118,7 +121,7 @@ struct Seg {
 };
 template <int NT> constexpr int kSegUsers = NT + 1 + 4 + 4 * NT;   // warps that release a slot: MMA, TMA of codes, converters, softmax
 
-static_assert(1024 + sizeof(Bars) + 2 * kExpSlots * 4 + kSegSlots * sizeof(Seg) + 8 <= 2048, "control block");
+static_assert(1024 + sizeof(Bars) + kExpWords * kExpSlots * 4 + kSegSlots * sizeof(Seg) + 8 <= 2048, "control block");
 
 struct PartHead {
   int32_t seq, hk, item, begin;
@@ -256,6 +259,246 @@ __device__ __forceinline__ uint32_t codes_h2(uint32_t v) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// A row's running maximum (log2), the sum of its weights (2^kBase per unit weight), and the units of its O.
+struct RowSum {
+  float m, l;
+  float evf;                     // log2 of the row's largest contribution so far, less m,
+  int evr;                       // rounded up: O is in units of 2^(m + evr - kBase)
+};
+// A step of a softmax warp: 64 keys of a tile.
+struct Step {
+  uint32_t tS, tO;               // the scores, which P replaces, and O in TMEM
+  uint64_t *pv_done;             // of the step before
+  uint32_t pv_parity;
+  int first;                     // of a segment: there is no O yet
+  int lim;                       // keys that the row sees
+  int ek, ev;                    // the block's K and V scales
+  float sc;                      // score factor
+  volatile int *abort_flag;
+  uint32_t *err;
+};
+
+// Moves m (and the units of O, evr) to what the step needs: mx its largest score, my its
+// largest score with the V scale, relative to 2^ev.
+template <int D>
+__device__ __forceinline__ bool take_max(RowSum &r, const Step &st, float mx, float my) {
+  const float m_new = fmaxf(r.m, mx);
+  // contributions of the row may pass the units of O by 2^kRescale
+  const bool need = m_new > r.m + kRescale || my + (float)(st.ev - r.evr) > r.m + kRescale;
+  if (__any_sync(0xffffffffu, need)) {
+    // O must be complete up to the step before.  (A barrier for each S buffer: the
+    // scores of step j came behind PV(j - 2), so the PV before on this one is over and
+    // its parity is not ambiguous.)
+    if (!st.first && !wait_warp(st.pv_done, st.pv_parity, st.abort_flag, st.err)) return false;
+    ptx::tc_fence_after();
+    // The new units: the larger of the old ones and the block's largest contribution (a row
+    // that has seen nothing has no old ones), relative to 2^m and with their fraction: whole
+    // octaves taken from the whole ones of the time before would gain up to one each time, and
+    // every row of the warp comes by whenever one of them needs it
+    const float was = r.m == -INFINITY ? -INFINITY : r.evf + (r.m - m_new);
+    if (m_new != -INFINITY) r.evf = fmaxf(was, (my - m_new) + (float)st.ev);
+    const int evn = (int)ceilf(r.evf);
+    const float am = r.m == -INFINITY ? 0.f : ptx::ex2(r.m - m_new);
+    const float alpha = r.m == -INFINITY ? 0.f : ptx::ex2((r.m - m_new) + (float)(r.evr - evn));
+    if (!st.first) {
+#pragma unroll 1
+      for (int cc = 0; cc < D / 32; ++cc) {
+        uint32_t o[32];
+        ptx::tmem_ld32(st.tO + cc * 32, o);
+        ptx::tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+        ptx::tmem_st32(st.tO + cc * 32, o);
+      }
+    }
+    r.l *= am;
+    r.m = m_new;
+    r.evr = evn;
+  }
+  return true;
+}
+
+// The step of a tile whose values carry their scales.  No key's contribution has a score above `most`.
+template <int D>
+__device__ __forceinline__ bool tile_step(RowSum &r, const Step &st, float most) {
+  uint32_t x[HN];
+  ptx::tmem_ld32(st.tS, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+  ptx::tmem_ld32(st.tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
+  ptx::tmem_ld_wait();
+  if (__any_sync(0xffffffffu, st.lim < HN)) {
+#pragma unroll
+    for (int i = 0; i < HN; ++i) x[i] = i < st.lim ? x[i] : 0xff800000u;
+  }
+  float mq[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) mq[q] = fmaxf(__uint_as_float(x[2 * q]), __uint_as_float(x[2 * q + 1]));
+#pragma unroll
+  for (int i = 8; i < HN; i += 8)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      mq[q] = ptx::fmax3(mq[q], __uint_as_float(x[i + 2 * q]), __uint_as_float(x[i + 2 * q + 1]));
+  const float mx = ptx::fmax3(mq[0], mq[1], fmaxf(mq[2], mq[3])) * st.sc;
+  if (!take_max<D>(r, st, mx, fminf(mx, most))) return false;
+  // values more than 2^64 below the row's units count as that small (the sum
+  // needs the weights above fp32's underflow)
+  const int dv = max(st.ev - r.evr, -64);
+  const float shift = (r.m == -INFINITY ? 0.f : -r.m) + (float)(kBase + dv);
+  const uint64_t scale2 = ptx::f2_pack(st.sc, st.sc);
+  const uint64_t shift2 = ptx::f2_pack(shift, shift);
+  uint64_t sp2[4] = {0, 0, 0, 0};
+  uint32_t pk[HN / 2];
+#pragma unroll
+  for (int i = 0; i < HN; i += 2) {
+    float a0, a1;
+    ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), scale2, shift2), a0, a1);
+    const float p0 = ptx::ex2(a0), p1 = ptx::ex2(a1);
+    sp2[(i >> 1) & 3] = ptx::f2_add(sp2[(i >> 1) & 3], ptx::f2_pack(p0, p1));
+    pk[i >> 1] = ptx::pack_f16_sat(p0, p1);
+  }
+  ptx::tmem_st32(st.tS, pk);
+  float sp[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) ptx::f2_unpack(sp2[k], sp[2 * k], sp[2 * k + 1]);
+  const float sum = ((sp[0] + sp[1]) + (sp[2] + sp[3])) + ((sp[4] + sp[5]) + (sp[6] + sp[7]));
+  r.l += sum * ptx::ex2((float)-dv);            // weights of this step carry 2^dv
+  return true;
+}
+
+// The steps of blocks that are marked, with V rows of zeros or scales far apart.  Functions of their
+// own and not inlined: such blocks are rare, and the softmax warps' loop is bound by its code's size
+// too (with them in line 8 prompts of 2048 tokens took 4 % longer).
+struct MarkedSum {
+  RowSum r;
+  int ok;
+};
+
+// V rows of zeros among the step's keys: bit i of word k (from bit `shift` on) is key 4 i + k.  Such a
+// key's weight counts in the sum but not for the units of O: it may pass them, by up to 2^kLift (so
+// that the sum does not overflow), and is cut off at fp16's largest value, which its zeros take to nothing.
+template <int D>
+__device__ __noinline__ MarkedSum zeros_step(RowSum r, const Step st, const int *words, int shift) {
+  uint32_t z[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) z[k] = (uint32_t)words[k] >> shift;
+  float mx = -INFINITY, my = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < HN; c += 8) {
+    uint32_t v[8];
+    ptx::tmem_ld8(st.tS + c, v, 0);
+    ptx::tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float y = c + i < st.lim ? __uint_as_float(v[i]) : -INFINITY;
+      mx = fmaxf(mx, y);
+      my = fmaxf(my, (z[i & 3] >> (i / 4)) & 1 ? -INFINITY : y);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) z[k] >>= 2;
+  }
+  const bool ok = tile_step<D>(r, st, fmaxf(my * st.sc, mx * st.sc - kLift));
+  return MarkedSum{r, ok};
+}
+
+// A wide tile, whose codes carry no scale.
+struct Wide {
+  const int *e;                  // what is published of the block
+  int shift;                     // the step's place in its words
+  int key0, end;                 // the step's first key; the keys that the row sees
+  const int32_t *pt;
+  const uint8_t *ks, *vs;
+  int hk, hkv, p, p_shift, num_pages;
+};
+template <int D>
+__device__ __noinline__ MarkedSum wide_step(RowSum r, const Step st, const Wide b) {
+  const int lim = st.lim;
+  const bool wide_k = (b.e[0] & kWideBit) != 0, wide_v = (b.e[1] & kWideBit) != 0, zeros = (b.e[1] & kZeroBit) != 0;
+  uint32_t z[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) z[k] = zeros ? (uint32_t)b.e[2 + k] >> b.shift : 0u;
+  // the scale byte of key i, -1 if it is not seen or its page is outside the pool
+  auto scale_byte = [&](const uint8_t *src, int i) -> int {
+    const int pos = b.key0 + i;
+    const int pg = pos < b.end ? b.pt[pos >> b.p_shift] : -1;
+    if (pg < 0 || pg >= b.num_pages) return -1;
+    return src[((size_t)pg * b.hkv + b.hk) * b.p + (pos & (b.p - 1))];
+  };
+  auto score = [&](uint32_t v, int i) -> float {
+    if (i >= lim) return -INFINITY;
+    const int d = wide_k ? min(scale_byte(b.ks, i) - st.ek, 0) : 0;   // > 0: a NaN key, NaN already
+    return __uint_as_float(v) * (d < -126 ? 0.f : __uint_as_float((uint32_t)(127 + d) << 23)) * st.sc;
+  };
+  // V scale of key i relative to `ref`; the tile's own where its values carry theirs
+  auto rel_ev = [&](int i, int ref) -> float { return (float)((wide_v ? scale_byte(b.vs, i) : st.ev) - ref); };
+  float mx = -INFINITY, my = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < HN; c += 8) {
+    uint32_t v[8];
+    ptx::tmem_ld8(st.tS + c, v, 0);
+    ptx::tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float y = score(v[i], c + i);
+      mx = fmaxf(mx, y);
+      if (!((z[i & 3] >> (c / 4 + i / 4)) & 1)) my = fmaxf(my, y + rel_ev(c + i, st.ev));
+    }
+  }
+  if (!take_max<D>(r, st, mx, fmaxf(my, mx - 300.f))) return MarkedSum{r, 0};
+  // the sum of the bare weights; P with each key's scale
+  const float shift = (r.m == -INFINITY ? 0.f : -r.m) + (float)kBase;
+  float sum = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < HN; c += 8) {
+    uint32_t v[8], pk[4];
+    ptx::tmem_ld8(st.tS + c, v, 0);
+    ptx::tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const float y0 = score(v[i], c + i) + shift;
+      const float y1 = score(v[i + 1], c + i + 1) + shift;
+      sum += ptx::ex2(y0) + ptx::ex2(y1);
+      pk[i / 2] = ptx::pack_f16_sat(ptx::ex2(y0 + rel_ev(c + i, r.evr)), ptx::ex2(y1 + rel_ev(c + i + 1, r.evr)));
+    }
+    ptx::tmem_st4(st.tS + c / 2, pk);            // behind what has been read
+  }
+  r.l += sum;
+  return MarkedSum{r, 1};
+}
+
+// Bytes of v that are the scale 2^0.
+__device__ __forceinline__ uint32_t has_one(uint32_t v) {
+  const uint32_t x = v ^ (kScaleOne * 0x01010101u);
+  return (x - 0x01010101u) & ~x & 0x80808080u;
+}
+// Which of a lane's four keys, at most `keys` of them, hold rows of zeros (of either sign): bit k is
+// the K row of key k, bit 4 + k its V row.  Byte k of ks and vs are their scales; their codes are `at`
+// + k * stride.  By the format a row of zeros has the scale 2^0, so only such rows are looked
+// through.  Not inlined: rare.
+template <int D>
+__device__ __noinline__ uint32_t zero_rows(const uint8_t *k_codes, const uint8_t *v_codes, size_t at, size_t stride,
+                                           uint32_t ks, uint32_t vs, int keys) {
+  auto some = [](const uint4 &v) { return ((v.x | v.y | v.z | v.w) & 0x7f7f7f7fu) != 0; };
+  auto row = [&](int i) { return (i < 4 ? k_codes : v_codes) + at + (i & 3) * stride; };
+  uint32_t mask = 0;
+  uint4 first[8];                                 // one latency
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const bool look = (i & 3) < keys && (((i < 4 ? ks : vs) >> (8 * (i & 3))) & 255u) == kScaleOne;
+    first[i] = look ? *reinterpret_cast<const uint4 *>(row(i)) : make_uint4(1, 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (!some(first[i])) mask |= 1u << i;
+#pragma unroll 1
+  for (uint32_t left = mask; left != 0; left &= left - 1) {   // the rest of those: one each
+    const int i = __ffs((int)left) - 1;
+    bool any = false;
+#pragma unroll
+    for (int q = 16; q < D; q += 16) any |= some(*reinterpret_cast<const uint4 *>(row(i) + q));
+    if (any) mask &= ~(1u << i);
+  }
+  return mask;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -272,8 +515,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint16_t *s_fac = reinterpret_cast<uint16_t *>(base + S::kData);   // [2][K, V][128] factors of a block's keys
   Bars *bars = reinterpret_cast<Bars *>(s_fac + 2 * 2 * BN);
   int64_t *s_scan = reinterpret_cast<int64_t *>(s_fac);          // [2 * 16 + 2], before the factors
-  int *s_exp = reinterpret_cast<int *>(bars + 1);             // [kExpSlots][2]
-  Seg *s_seg = reinterpret_cast<Seg *>(s_exp + 2 * kExpSlots);   // [kSegSlots]
+  int *s_exp = reinterpret_cast<int *>(bars + 1);             // [kExpSlots][kExpWords]
+  Seg *s_seg = reinterpret_cast<Seg *>(s_exp + kExpWords * kExpSlots);   // [kSegSlots]
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_seg + kSegSlots);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
@@ -473,6 +716,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = queue(0, load, bytes, hk, row);
           if (!ok) break;
           ++queued;
+          const uint32_t ksn = scales_of(j + 1, pgn, a.c.ks), vsn = scales_of(j + 1, pgn, a.c.vs);
+          // Rows of zeros have a scale that says nothing of their size: they do not count for the block's
+          // scales (their bytes become 255 here), and the softmax warps are told of the V rows.
+          uint32_t real = 15, zero_bit = 0;              // real: keys whose NaN scales are that
+          if (__builtin_expect(__any_sync(0xffffffffu, (has_one(ks) | has_one(vs)) != 0), 0)) {
+            const int lpos = (b0 + j) * BN + lane * 4, keys = (unsigned)pg < (unsigned)a.num_pages ? kv - lpos : 0;
+            const size_t stride = (size_t)a.hkv * D;
+            const size_t at = keys > 0 ? ((size_t)pg * a.p + (lpos & (a.p - 1))) * stride + (size_t)hk * D : 0;
+            const uint32_t zero = zero_rows<D>(a.c.k, a.c.v, at, stride, ks, vs, keys);
+            real = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (((ks >> (8 * k)) & 255u) == kScaleNan || ((vs >> (8 * k)) & 255u) == kScaleNan) real |= 1u << k;
+              if ((zero >> k) & 1) ks |= 255u << (8 * k);
+              if ((zero >> (4 + k)) & 1) vs |= 255u << (8 * k);
+              const uint32_t word = __ballot_sync(0xffffffffu, (zero >> (4 + k)) & 1);
+              if (word != 0) zero_bit = kZeroBit;
+              // free, as below
+              if (lane == 0) s_exp[(gb % kExpSlots) * kExpWords + 2 + k] = (int)word;
+            }
+          }
           // the block's largest and smallest scales over the keys it has; NaN scales mark the key
           uint32_t nans = 0;
           int ek = 0, ev = 0, ek0 = 255, ev0 = 255;
@@ -484,6 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (key && k8 != (int)kScaleNan) ek = max(ek, k8), ek0 = min(ek0, k8);
             if (key && v8 != (int)kScaleNan) ev = max(ev, v8), ev0 = min(ev0, v8);
           }
+          nans &= real;
           ek = __reduce_max_sync(0xffffffffu, ek);
           ev = __reduce_max_sync(0xffffffffu, ev);
           const bool wk = ek - __reduce_min_sync(0xffffffffu, ek0) > kWide;
@@ -505,8 +770,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) {
             // free: the K tile of block gb - 1 is converted, so QK of block gb - 5 or a later one
             // is done for both tiles, and was issued behind the P of every block before it
-            s_exp[(gb % kExpSlots) * 2] = ek | (wk ? kWideBit : 0);
-            s_exp[(gb % kExpSlots) * 2 + 1] = ev | (wv ? kWideBit : 0);
+            s_exp[(gb % kExpSlots) * kExpWords] = ek | (wk ? kWideBit : 0);
+            s_exp[(gb % kExpSlots) * kExpWords + 1] = ev | (wv ? kWideBit : 0) | (int)zero_bit;
           }
           __syncwarp();
           if (lane == 0) {
@@ -517,8 +782,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           ++queued;
           pg = pgn;
-          ks = scales_of(j + 1, pg, a.c.ks);
-          vs = scales_of(j + 1, pg, a.c.vs);
+          ks = ksn;
+          vs = vsn;
         }
       }
       // queued copies land before the CTA ends
@@ -744,169 +1009,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t *pt = c.pt;
       const float qf = c.qf;
       int ek = 0, ev = 0;
-      bool wide_k = false, wide_v = false;
-      float m = -INFINITY, l = 0.f;                   // l counts 2^kBase per unit weight
-      float evf = 0.f;                                // log2 of the row's largest contribution so far, less m,
-      int evr = 0;                                    // rounded up: O is in units of 2^(m + evr - kBase)
+      int marks = 0;                                  // of the block: kWideBit, kZeroBit
+      RowSum r{-INFINITY, 0.f, 0.f, 0};
       for (int j = 0; j < nt; ++j) {                  // steps
         const int blk = gb + j / SPB, eslot = blk % kExpSlots, buf = (gt + j) & 1;
         const uint32_t tS = lane_base + (uint32_t)(t * 128 + buf * HN);
         if (j % SPB == 0) {                           // a new block's scales
+          // (A tile that skipped blocks cannot come by here eight blocks early, when the barrier's
+          // parity would pass: tile 0 skips one block at most, at a run's begin; tile 1's Q is
+          // loaded behind tile 0's, which waits for every QK of the segment before.)
           ok = wait_warp(&bars->e_full[eslot], (uint32_t)((blk / kExpSlots) & 1), abort_flag, err);
-          ek = s_exp[eslot * 2];
-          ev = s_exp[eslot * 2 + 1];
-          wide_k = ek >= kWideBit;
-          wide_v = ev >= kWideBit;
+          ek = s_exp[eslot * kExpWords];
+          ev = s_exp[eslot * kExpWords + 1];
+          marks = ek | ev;
           ek &= 255;
           ev &= 255;
         }
         ok = ok && wait_warp(&bars->s_full[t][buf], (uint32_t)(((gt + j) >> 1) & 1), abort_flag, err);
         if (!ok) break;
         const int key0 = b0 * BN + j * HN;            // the step's first key
-        // For a wide tile (whose codes carry no scale): the scale byte of key i, -1 if it
-        // is not seen or its page is outside the pool
-        auto scale_byte = [&](const uint8_t *src, int i) -> int {
-          const int pos = key0 + i;
-          const int pg = pos < end ? pt[pos >> a.p_shift] : -1;
-          if (pg < 0 || pg >= a.num_pages) return -1;
-          return src[((size_t)pg * a.hkv + hk) * a.p + (pos & (a.p - 1))];
-        };
-        auto wide_score = [&](const uint32_t (&v)[8], int vi, int i, int lim, float sc, int top) -> float {
-          if (i >= lim) return -INFINITY;
-          const int d = wide_k ? min(scale_byte(a.c.ks, i) - top, 0) : 0;   // > 0: a NaN key, NaN already
-          return __uint_as_float(v[vi]) * (d < -126 ? 0.f : __uint_as_float((uint32_t)(127 + d) << 23)) * sc;
-        };
-        // V scale of key i relative to `ref`; the tile's own `top` where its values carry theirs
-        auto wide_ev = [&](int i, int top, int ref) -> float {
-          return (float)((wide_v ? scale_byte(a.c.vs, i) : top) - ref);
-        };
         ptx::tc_fence_after();
-        const int lim = min(HN, end - key0);
         // never 0, which would make NaN of a masked score
         float sc = qf * scale_value((uint32_t)ek);
         if (sc < 1e-37f) sc = 1e-37f;
-        // Moves m (and the units of O, evr) to what the block needs: mx its largest score, my
-        // its largest score with the V scale, relative to 2^ev.
-        auto take_max = [&](float mx, float my) -> bool {
-          const float m_new = fmaxf(m, mx);
-          // contributions of the row may pass the units of O by 2^kRescale
-          const bool need = m_new > m + kRescale || my + (float)(ev - evr) > m + kRescale;
-          if (__any_sync(0xffffffffu, need)) {
-            // O must be complete up to the step before.  (A barrier for each S buffer: the
-            // scores of step j came behind PV(j - 2), so the PV before on this one is over and
-            // its parity is not ambiguous.)
-            if (j > 0 && !wait_warp(&bars->pv_done[t][buf ^ 1], (uint32_t)(((gt + j - 1) >> 1) & 1), abort_flag, err))
-              return false;
-            ptx::tc_fence_after();
-            // The new units: the larger of the old ones and the block's largest contribution (a row
-            // that has seen nothing has no old ones), relative to 2^m and with their fraction: whole
-            // octaves taken from the whole ones of the time before would gain up to one each time, and
-            // every row of the warp comes by whenever one of them needs it
-            const float was = m == -INFINITY ? -INFINITY : evf + (m - m_new);
-            if (m_new != -INFINITY) evf = fmaxf(fmaxf(was, (my - m_new) + (float)ev), -300.f);
-            const int evn = (int)ceilf(evf);
-            const float am = m == -INFINITY ? 0.f : ptx::ex2(m - m_new);
-            const float alpha = m == -INFINITY ? 0.f : ptx::ex2((m - m_new) + (float)(evr - evn));
-            if (j > 0) {
-#pragma unroll 1
-              for (int cc = 0; cc < D / 32; ++cc) {
-                uint32_t r[32];
-                ptx::tmem_ld32(tO + cc * 32, r);
-                ptx::tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
-                ptx::tmem_st32(tO + cc * 32, r);
-              }
-            }
-            l *= am;
-            m = m_new;
-            evr = evn;
-          }
-          return true;
-        };
-        // values more than 2^64 below the row's units count as that small (the sum
-        // needs the weights above fp32's underflow)
-        auto lift = [&]() -> int { return max(ev - evr, -64); };
-        if (__builtin_expect(!(wide_k || wide_v), 1)) {   // the same for the whole tile
-          uint32_t x[HN];
-          ptx::tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
-          ptx::tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
-          ptx::tmem_ld_wait();
-          if (__any_sync(0xffffffffu, lim < HN)) {
-#pragma unroll
-            for (int i = 0; i < HN; ++i) x[i] = i < lim ? x[i] : 0xff800000u;
-          }
-          float mq[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) mq[q] = fmaxf(__uint_as_float(x[2 * q]), __uint_as_float(x[2 * q + 1]));
-#pragma unroll
-          for (int i = 8; i < HN; i += 8)
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              mq[q] = ptx::fmax3(mq[q], __uint_as_float(x[i + 2 * q]), __uint_as_float(x[i + 2 * q + 1]));
-          const float mx = ptx::fmax3(mq[0], mq[1], fmaxf(mq[2], mq[3])) * sc;
-          if (!take_max(mx, mx)) {
-            ok = false;
-            break;
-          }
-          const int dv = lift();
-          const float shift = (m == -INFINITY ? 0.f : -m) + (float)(kBase + dv);
-          const uint64_t scale2 = ptx::f2_pack(sc, sc);
-          const uint64_t shift2 = ptx::f2_pack(shift, shift);
-          uint64_t sp2[4] = {0, 0, 0, 0};
-          uint32_t pk[HN / 2];
-#pragma unroll
-          for (int i = 0; i < HN; i += 2) {
-            float a0, a1;
-            ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), scale2, shift2), a0,
-                           a1);
-            const float p0 = ptx::ex2(a0), p1 = ptx::ex2(a1);
-            sp2[(i >> 1) & 3] = ptx::f2_add(sp2[(i >> 1) & 3], ptx::f2_pack(p0, p1));
-            pk[i >> 1] = ptx::pack_f16(p0, p1);
-          }
-          ptx::tmem_st32(tS, pk);
-          float sp[8];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) ptx::f2_unpack(sp2[k], sp[2 * k], sp[2 * k + 1]);
-          const float sum = ((sp[0] + sp[1]) + (sp[2] + sp[3])) + ((sp[4] + sp[5]) + (sp[6] + sp[7]));
-          l += sum * ptx::ex2((float)-dv);            // weights of this step carry 2^dv
+        const Step st{tS, tO, &bars->pv_done[t][buf ^ 1], (uint32_t)(((gt + j - 1) >> 1) & 1), j == 0,
+                      min(HN, end - key0), ek, ev, sc, abort_flag, err};
+        if (__builtin_expect(marks < kWideBit, 1)) {
+          ok = tile_step<D>(r, st, INFINITY);
         } else {
-          float mx = -INFINITY, my = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < HN; c += 8) {
-            uint32_t v[8];
-            ptx::tmem_ld8(tS + c, v, 0);
-            ptx::tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float y = wide_score(v, i, c + i, lim, sc, ek);
-              mx = fmaxf(mx, y);
-              my = fmaxf(my, y + wide_ev(c + i, ev, ev));
-            }
-          }
-          if (!take_max(mx, my)) {
-            ok = false;
-            break;
-          }
-          // the sum of the bare weights; P with each key's scale
-          const float shift = (m == -INFINITY ? 0.f : -m) + (float)kBase;
-          float sum = 0.f;
-#pragma unroll 1
-          for (int c = 0; c < HN; c += 8) {
-            uint32_t v[8], pk[4];
-            ptx::tmem_ld8(tS + c, v, 0);
-            ptx::tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-              const float y0 = wide_score(v, i, c + i, lim, sc, ek) + shift;
-              const float y1 = wide_score(v, i + 1, c + i + 1, lim, sc, ek) + shift;
-              sum += ptx::ex2(y0) + ptx::ex2(y1);
-              pk[i / 2] = ptx::pack_f16(ptx::ex2(y0 + wide_ev(c + i, ev, evr)), ptx::ex2(y1 + wide_ev(c + i + 1, ev, evr)));
-            }
-            ptx::tmem_st4(tS + c / 2, pk);            // behind what has been read
-          }
-          l += sum;
+          const int *e = s_exp + eslot * kExpWords;
+          const int shift = j % SPB * (HN / 4);
+          const MarkedSum ms = marks & kWideBit
+                                   ? wide_step<D>(r, st, Wide{e, shift, key0, end, pt, a.c.ks, a.c.vs, hk, a.hkv, a.p,
+                                                              a.p_shift, a.num_pages})
+                                   : zeros_step<D>(r, st, e + 2, shift);
+          r = ms.r;
+          ok = ms.ok != 0;
         }
+        if (!ok) break;
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
         ptx::mbar_arrive(&bars->p_full[t][buf]);
@@ -924,12 +1064,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ptx::tc_fence_after();
       if (end == 0) {                                 // sees no key, whatever its q holds
-        l = 0.f;
-        m = -INFINITY;
+        r.l = 0.f;
+        r.m = -INFINITY;
       }
-      // O / l is in units of 2^(evr - 127); a part keeps O in them
-      const float unit = ptx::ex2((float)(evr - 127));
-      const float mul = end == 0 ? 0.f : !c.whole ? unit : l == 0.f ? 0.f : unit / l;
+      // O / l is in units of 2^(evr - 127), which may be below ex2's smallest; a part keeps O in them
+      const float unit = r.evr < 64 ? ptx::ex2((float)(r.evr - 63)) * 0x1p-64f : ptx::ex2((float)(r.evr - 127));
+      const float mul = end == 0 ? 0.f : !c.whole ? unit : r.l == 0.f ? 0.f : unit / r.l;
       const uint64_t mul2 = ptx::f2_pack(mul, mul);
       const bool blank = __any_sync(0xffffffffu, end == 0);   // a row of the warp sees no key: its O is dropped
       const uint64_t once = ptx::l2_evict_first_policy();
@@ -969,9 +1109,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (c.mine) {
         if (!c.whole)
-          g.ml[c.slot * S::ROWS + t * 128 + row] = make_float2(m, l);
+          g.ml[c.slot * S::ROWS + t * 128 + row] = make_float2(r.m, r.l);
         else if (a.lse != nullptr)
-          a.lse[c.at] = l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l) - kBase) * kLn2;
+          a.lse[c.at] = r.l == 0.f ? -INFINITY : ((r.m == -INFINITY ? 0.f : r.m) + log2f(r.l) - kBase) * kLn2;
       }
       c = next;
     }

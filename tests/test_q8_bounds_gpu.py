@@ -33,13 +33,13 @@ def test_attend(name, dtype):
 # size of the values beside the row of zeros; how far its score is above the others'
 @pytest.mark.parametrize("size,lift", [(1.0, 8.0), (1e-4, 8.0), (1e-6, 8.0), (1e-6, -8.0), (1e-6, 0.0), (1e-3, 25.0)])
 @pytest.mark.parametrize("d", [64, 128, 256])
-@pytest.mark.parametrize("dtype,q_len", [(BF16, 4), (F32, 4), (F32, 40)])
+@pytest.mark.parametrize("dtype,q_len", [(BF16, 4), (BF16, 40), (BF16, 150), (F32, 4), (F32, 40)])
 def test_rows_of_zeros_do_not_coarsen_the_others(dtype, q_len, d, size, lift):
     pr = Q.zero_sink(dtype, size, q_len=q_len, kv_len=333, hq=4, hkv=2, d=d, lift=lift, n=2)
     Dev(pr).attend().checked(Q.attend(pr), what=f"values of {size}")
 
 
-@pytest.mark.parametrize("name", ["decode", "decode_d256", "decode_g16", "few", "one"])
+@pytest.mark.parametrize("name", ["decode", "decode_d256", "decode_g16", "few", "one", "chunk", "chunk_d64", "chunk_d256", "cross_gqa", "fresh"])
 def test_scattered_rows_of_zeros(name):
     """Rows of zeros (of both signs) and rows at scale 2^0 or the smallest one that are not zeros
     but for a late value, among small ones."""
