@@ -441,7 +441,9 @@ RPA_API int rpa_host_groups(const int32_t *cu_q_lens, int32_t num_seqs,
  * 448 * 2^e (0 for a row of zeros) and code_d = x_d * 2^-e rounded to the
  * nearest e4m3 value, ties to even.  x_d * 2^-e is exact, so a code is off by one
  * rounding: at most 2^-4 of the value, or 2^-10 * 2^e for values below
- * 2^-6 * 2^e.  The row stands for code_d * 2^e.  A row with an infinity or a
+ * 2^-6 * 2^e.  (At e = 120, the largest, a code stops at 240, since 256 * 2^120 is
+ * an infinity: finite rows stay finite, still within 2^-4.)  The row stands for
+ * code_d * 2^e.  A row with an infinity or a
  * NaN gets the NaN scale and zero codes: it stands for NaN throughout.  Codes
  * written by the library are never NaN; what the operators make of a NaN code
  * (0x7f, 0xff) that something else wrote is unspecified.

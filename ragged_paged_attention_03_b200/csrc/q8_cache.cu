@@ -191,7 +191,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks<T>) io_kernel(const IoArgs a
           ptx::f2_unpack(ptx::f2_mul(pair(x[v], 2 * i + 1), inv2), f[2], f[3]);
           w[i] = to_e4m3x2(f[0], f[1]) | (to_e4m3x2(f[2], f[3]) << 16);
         }
-        if (code == kScaleNan) w[0] = w[1] = w[2] = w[3] = 0;
+        if (code >= kScaleTop) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = code == kScaleNan ? 0u : below_2_128(w[i]);
+        }
         *reinterpret_cast<uint4 *>((v ? a.c.v : a.c.k) + crow) = make_uint4(w[0], w[1], w[2], w[3]);
         if (sub == 0) (v ? a.c.vs : a.c.ks)[srow] = (uint8_t)code;
       }

@@ -11,7 +11,9 @@
 // own, so a finer scale would not make them more precise, only use the last
 // fraction of a binade at the top.  The scale is stored as the byte e + 127
 // (e8m0); 255 is NaN and marks a row that held an infinity or a NaN, whose codes
-// are zeros: a stored code is never NaN.
+// are zeros: a stored code is never NaN.  At the largest scale, 2^120, codes stop at 240: the next one,
+// 256, would stand for 2^128, an infinity in both row types (240 is within half a step, 2^-4, of every
+// finite value that would round to it).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -24,6 +26,7 @@ namespace q8 {
 
 constexpr uint32_t kScaleOne = 127;
 constexpr uint32_t kScaleNan = 255;
+constexpr uint32_t kScaleTop = 247;   // 2^120, the largest of a finite row
 
 struct Cache {
   uint8_t *k, *v;     // codes [num_pages, P, Hkv, D]
@@ -186,6 +189,10 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
+}
+// Four codes at the scale kScaleTop: 256 becomes 240, of either sign.
+__device__ __forceinline__ uint32_t below_2_128(uint32_t v) {
+  return v - (__vcmpeq4(v & 0x7f7f7f7fu, 0x78787878u) & 0x01010101u);
 }
 // Two e4m3 codes (low 16 bits) to fp16 (exact).
 __device__ __forceinline__ __half2 from_e4m3x2(uint32_t v) {

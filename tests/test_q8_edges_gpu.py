@@ -101,3 +101,38 @@ def test_rows_beside_one_whose_maximum_climbs(d, fade):
     pr = replace(pr, q_lens=pr.q_lens * times, kv_lens=pr.kv_lens * times, table=pr.table.repeat(times, 1),
                  q=pr.q.repeat(times, 1, 1))
     Dev(pr).attend().checked([x.repeat(times, *[1] * (x.dim() - 1)) for x in ref], what=f"head_dim {d}")
+
+
+@pytest.mark.parametrize("dtype", [BF16, torch.float32])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_the_largest_finite_rows_stay_finite(d, dtype):
+    """Values up to the types' largest: the codes that would stand for 2^128 are those below."""
+    pr = R.make([40], [40], hq=2, hkv=2, d=d, p=16, dtype=dtype, seed=1)
+    gen = torch.Generator().manual_seed(8)
+    rows = []
+    for i in range(2):
+        x = (torch.rand(40, 2, d, generator=gen) * 2 - 1) * torch.finfo(dtype).max
+        x[0] = torch.finfo(dtype).max
+        x[1] = -torch.finfo(dtype).max
+        x[2, :, ::2] = 248.0 * 2.0 ** 120                      # half way between 240 and 256
+        x[3] = torch.linspace(200.0, 255.0, d) * 2.0 ** 120
+        x[4] = 448.0 * 2.0 ** 119                              # the largest of the scale below
+        rows.append(x.to(dtype))
+    assert all(torch.isfinite(x).all() for x in rows)
+    dv = Dev(pr)
+    dv.rb.rpa_q8_write(rows[0].cuda(), rows[1].cuda(), *dv.cache, dev_flags=dv.flags)
+    back = [torch.empty_like(r, device="cuda") for r in rows]
+    dv.rb.rpa_q8_read(*back, *dv.cache, dev_flags=dv.flags)
+    assert int(dv.flags.item()) == 0
+    page, slot = places(pr, 0, torch.arange(40))
+    for x, got, codes, scales in zip(rows, back, (dv.kc, dv.vc), (dv.ks, dv.vs)):
+        c, e = R.quantise_row(x)
+        top = (e == 247)[..., None] & ((c & 0x7F) == 0x78)
+        assert top.any() and (e == 246).any()
+        c = torch.where(top, c - 1, c)
+        assert torch.equal(codes.view(torch.uint8).cpu()[page, slot], c)
+        assert torch.equal(scales.view(torch.uint8).cpu()[page, :, slot], e)
+        got = got.double().cpu()
+        assert torch.equal(got, R.E4M3[c.long()] * R.scale_of(e)[..., None]) and torch.isfinite(got).all()
+        err = (got - x.double()).abs()
+        assert (err <= torch.maximum(x.double().abs() * 2.0 ** -4, R.scale_of(e)[..., None] * 2.0 ** -10)).all()
