@@ -512,14 +512,25 @@ RPA_API int rpa_q8_workspace_size(const rpa_dims *dims, int32_t max_seqs,
                                   int32_t max_q_len, int64_t *bytes);
 
 /*
- * rpa_q8_attend -- exact attention of ragged queries over the cached keys.
+ * rpa_q8_attend -- attention of ragged queries over the cached keys, every
+ * visible key counted.
  *
  *   q, out [T, Hq, D], lse [T, Hq] float32 or NULL.  Query row cu_q_lens[s] + i,
  *   head h sees positions j < kv_len[s] of KV head h / G and, when causal != 0,
  *   only j <= kv_len[s] - q_len[s] + i (aligned to the end):
  *   out = sum_j softmax_j(scale * q.k_j) v_j and lse = ln sum_j exp(scale *
- *   q.k_j) with k_j, v_j the values that the cached rows stand for, held in
- *   fp32 and out rounded once.
+ *   q.k_j) with k_j, v_j the values that the cached rows stand for, taken as
+ *   they are.  Sums, maxima and lse are held in fp32 and out is rounded once;
+ *   what enters the products has fewer bits where dtype is RPA_BF16:
+ *     weights  16 rows or fewer per KV head (q_len * G): off by 2^-19 of the weight
+ *              at most; more rows: by 2^-11 (fp16).  fp32: by 2^-24 or less
+ *     q        exact down to 2^-12 of the row's largest value, and within 2^-21
+ *              of that below.  fp32: off by 2^-24 of the value, or 2^-37 of the largest
+ *   A weight counts relative to the row's largest weight times V scale (rows of
+ *   zeros, of scale 2^0 as the format has them, aside), down to 2^-29 of it (2^-38
+ *   for fp32).  Weights times values are summed before the division by the weights'
+ *   sum: values above 2^120 over the number of keys may overflow, and
+ *   contributions below 2^-110 may be lost.
  *   The keys are all in the cache: new tokens are written by rpa_q8_write
  *   first and attended to as stored.  Any kv_len >= 0 is allowed for any
  *   q_len: with causal == 0 this is cross attention to cached states of

@@ -8,20 +8,20 @@
 // e4m3 codes into fp16 (64 a clock and SM measured, against 32 for the shifts and
 // masks that make bf16 of them), and P has 11 bits instead of 8.  Ranges are
 // kept by powers of two, which are exact:
-//   K tile:  code * 2^(ek - ekb), ekb the largest K scale of the 128 keys; the
-//            factor 2^ekb joins the row's score factor;
+//   K tile:  code * 2^(ek - ekb), ekb the largest K scale of the 128 keys (but for rows of
+//            zeros); the factor 2^ekb joins the row's score factor;
 //   V tile:  code * 2^(ev - evb) the same way; P of the block carries 2^(evb - evr)
 //            in its exponent, evr the row's own reference, moved (with a rescale of
 //            the row's O) when its contributions pass it by more than 2^6;
 //   both exact while the tile's scales lie within 2^15 of each other.  A "wide" tile,
 //            whose scales do not, holds the bare codes, and the softmax warps apply the
 //            scales in fp32, key by key, from global memory (slow, and rare: rows of
-//            one sequence that differ in size by more than 30,000 times);
+//            one sequence, zeros aside, that differ in size by more than 30,000 times);
 //   Q row:   q * 2^-eq, as the cache's rows are scaled, so every value is exact
-//            down to 2^-33 of the row's largest;
-//   P:       2^5 at the row's largest weight times V scale (up to 2^11 while the
+//            down to 2^-25 of the row's largest and within 2^-33 of that below;
+//   P:       2^5 at the row's largest weight times its tile's V scale (up to 2^11 while the
 //            rescale is put off), so it has 11 bits down to 2^-19 of that and counts
-//            down to 2^-29.
+//            down to 2^-29.  Keys whose V rows are zeros do not set this unit.
 // A token whose K or V row is NaN gets a NaN key and a zero value: its column is
 // NaN for the rows that see it, and a masked column is dropped whatever it holds.
 //
@@ -33,12 +33,13 @@
 // Roles (512 threads of at most 128 registers).  Every hot loop is short and
 // rolled: with five kinds of warps on an SM the unrolled forms (a row's 128 scores in
 // registers) were bound by instruction fetch, at a third of this speed.
-// Measured (Hq 32, Hkv 8, D 128): 8 prompts of 2048 tokens 407 us (676 TFLOP/s of the causal
-// products), 4 chunks of 512 behind contexts of some thousands 195 us (725 TFLOP/s).  A block of
+// Measured (Hq 32, Hkv 8, D 128): 8 prompts of 2048 tokens 408 us (674 TFLOP/s of the causal
+// products), 4 chunks of 512 behind contexts of some thousands 195 us (725 TFLOP/s); D 256 (Hq 16,
+// Hkv 4), 4 prompts of 4096 tokens 941 us (584 TFLOP/s).  A block of
 // 128 keys takes 4,200 to 4,900 clocks where its MMAs need 2,048: the conversion of its K and V takes
 // the converters 4,200 (1,250 each, the rest waits that are over when they are looked at), a
 // softmax step 2,000 to 2,500 of which the exponentials are 650 to 1,200, by whether both
-// tiles' are at theirs; the tensor pipe is active 36 % of the time, the issue slots 52 %.
+// tiles' are at theirs; the tensor pipe is active 35 % of the time, the issue slots 51 %.
 //   warps 0-3, 4-7  softmax and output of tile 0 and 1 (one row per thread); they
 //                   also turn their tile's Q, landed by TMA as bf16, into scaled
 //                   fp16 in place
@@ -47,7 +48,9 @@
 //                   took 4,500 clocks for a step of the two tiles, waits that
 //                   were over included, and held everything else up
 //   warp 13         walks the run: writes its segments down for the others; TMA of Q
-//   warp 14         TMA of the code tiles; the scales of their keys as fp16 factors
+//   warp 14         TMA of the code tiles; the scales of their keys as fp16 factors; looks
+//                   for rows of zeros among those of scale 2^0 (8 prompts of 2048 tokens take
+//                   480 us where every row has that scale, 790 us with a V row of zeros in every block)
 // TMEM (512 columns): S/P of tile 0 (two buffers of 64 keys) | of tile 1 | O of
 // tile 0 | O of tile 1.
 #include <cuda.h>

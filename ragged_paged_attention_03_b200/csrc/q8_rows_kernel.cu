@@ -10,19 +10,19 @@
 //   O^T[D x R]       += V^T P^T    A = V codes, M-major, the same
 // in kind::f8f6f4, whose B operand must be 8 bits too.  Q and the weights P
 // are therefore written as sums of e4m3 parts, part i scaled by 16^i:
-// each part takes 4 bits of the significand, and the remainder of a rounding is
-// exact in fp32, so
-//   bf16 I/O: 2 parts of Q (exact down to 2^-21 of the row's largest |q|),
-//             4 of P (16 bits; weights down to 2^-30 of the row's largest count,
-//             so a long flat tail behind one large weight keeps its sum);
-//   fp32 I/O: 6 parts of both (24 bits, as the fp32 values they come from).
+// the remainder of a rounding is exact in fp32 and half a step at most, so that n parts
+// are off by 2^-(5 n - 1) of the value, while their last one is not below e4m3's smallest:
+//   bf16 I/O: 2 parts of Q (exact for values down to 2^-12 of the row's largest |q|, within
+//             2^-21 of that below), 4 of P (2^-19; weights down to 2^-30 of the row's largest
+//             count, so a long flat tail behind one large weight keeps its sum);
+//   fp32 I/O: 6 parts of both (five would hold 24 bits of the larger values).
 // The parts are columns of the same MMA (N = parts * R, whose time below
 // N = 64 is that of reading A), and their products are joined in fp32.
 // Scales: a key's K scale multiplies its score and its V scale its weight; one
 // thread owns one key, so both are a scalar of that thread.  A weight with its V
 // scale, exp2(x + ev), is taken relative to the largest of its row and block
-// (times 256) before the rounding to parts: keys that a row does not see, or whose
-// weight is small, do not coarsen it however large their values are.
+// (times 256) before the rounding to parts: keys that a row does not see, whose
+// weight is small, or whose V row is zeros, do not coarsen it however large their scales are.
 // Softmax: running maximum and sum in fp32 (log2 domain).  Each block's product
 // O^T is read from TMEM into fp32 registers, which are rescaled when the
 // maximum moves: no read-modify-write of TMEM and no wait between blocks.
@@ -43,9 +43,10 @@
 // 5 MMA issue, 6 the scales (cp.async).  4 and 6 run ahead across groups through
 // rings in shared memory.
 //
-// Measured: 128 single tokens behind 1024 to 8192 keys (Hq 32, Hkv 8, D 128) 167 us, 5.9 TB/s of
+// Measured: 128 single tokens behind 1024 to 8192 keys (Hq 32, Hkv 8, D 128) 168 us, 5.9 TB/s of
 // the cache's bytes, 0.90 of a plain copy's rate (986 MB read where 985 are needed); contexts up to
-// 131072 at D 256 318 us, 6.8 TB/s.  Single tokens in fp32 cost the six parts' columns, not bytes.
+// 131072 at D 256 320 us, 6.7 TB/s.  fp32 single tokens of the same lengths run at 5.3 TB/s; every
+// 8 fp32 rows of a KV head pass over its keys once more (4 chunks of 512 behind contexts 2.3 ms).
 #include <cuda.h>
 #include <limits.h>
 #include <math.h>
