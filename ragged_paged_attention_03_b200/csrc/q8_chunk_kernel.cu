@@ -341,7 +341,8 @@ __device__ __forceinline__ bool tile_step(RowSum &r, const Step &st, float most)
     for (int q = 0; q < 4; ++q)
       mq[q] = ptx::fmax3(mq[q], __uint_as_float(x[i + 2 * q]), __uint_as_float(x[i + 2 * q + 1]));
   const float mx = ptx::fmax3(mq[0], mq[1], fmaxf(mq[2], mq[3])) * st.sc;
-  if (!take_max<D>(r, st, mx, fminf(mx, most))) return false;
+  // (not fminf: a row of the tile that is no query holds anything, and NaN must not pass for `most`)
+  if (!take_max<D>(r, st, mx, most < mx ? most : mx)) return false;
   // values more than 2^64 below the row's units count as that small (the sum
   // needs the weights above fp32's underflow)
   const int dv = max(st.ev - r.evr, -64);

@@ -136,3 +136,25 @@ def test_the_largest_finite_rows_stay_finite(d, dtype):
         assert torch.equal(got, R.E4M3[c.long()] * R.scale_of(e)[..., None]) and torch.isfinite(got).all()
         err = (got - x.double()).abs()
         assert (err <= torch.maximum(x.double().abs() * 2.0 ** -4, R.scale_of(e)[..., None] * 2.0 ** -10)).all()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("hq,hkv,causal", [(10, 2, False), (6, 2, True), (14, 2, True), (10, 2, True)])
+def test_rows_of_a_tile_without_a_query_do_not_matter(hq, hkv, causal, d):
+    """A G that does not divide 128 leaves rows of a tile without a query: what a call before left there
+    (in every SM, at G = 1, where a tile has none) changes no bit."""
+    pr = R.make([171, 172, 180, 103], [946, 262, 194, 1489], hq=hq, hkv=hkv, d=d, p=32, causal=causal, seed=6,
+                scale=0.19 / d ** 0.5)
+    pr.q[:] = pr.q.abs()
+    pr.k_codes &= 0x7F                              # all scores positive, some far above others
+    before = Dev(R.make([300] * 80, [300] * 80, hq=2, hkv=2, d=d, p=32, causal=False, seed=7))
+    before.q.fill_(0.0)
+    before.attend()
+    dv = Dev(pr).attend()
+    first = dv.out.clone(), dv.lse.clone()
+    for fill in (torch.nan, 1e30, 1.0, torch.inf):
+        before.q.fill_(fill)
+        before.attend()
+        dv.out.fill_(77.0)
+        dv.attend()
+        assert torch.equal(dv.out, first[0]) and torch.equal(dv.lse, first[1]), f"after queries of {fill}"
