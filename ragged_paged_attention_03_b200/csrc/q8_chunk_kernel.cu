@@ -75,7 +75,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 6.0f;    // lazy rescale of O: weights reach 2^(6 + kBase)
 constexpr int kBase = 5;
 constexpr int kWide = 15;           // a tile whose scales spread further is "wide"
-constexpr int kLift = 100;          // weights whose V rows are zeros pass the units of O by 2^kLift at most
+constexpr int kLift = 24;           // weights whose V rows are zeros pass the units of O by 2^kLift at most
 constexpr int kWideBit = 1 << 16;   // in the published ekb / evb
 constexpr int kZeroBit = 1 << 17;   // in the published evb: the tile has V rows of zeros
 constexpr int kExpWords = 6;        // published of a block: ekb, evb, V rows of zeros (word k: keys 4 i + k)
@@ -377,8 +377,10 @@ struct MarkedSum {
 };
 
 // V rows of zeros among the step's keys: bit i of word k (from bit `shift` on) is key 4 i + k.  Such a
-// key's weight counts in the sum but not for the units of O: it may pass them, by up to 2^kLift (so
-// that the sum does not overflow), and is cut off at fp16's largest value, which its zeros take to nothing.
+// key's weight counts in the sum but not for the units of O: it may pass them, and is cut off at
+// fp16's largest value, which its zeros take to nothing.  By up to 2^kLift: exp2's argument, in which a
+// weight's distance from the unit is added, keeps 2^-20 of a weight up to there (2^-18 at 2^100), and the other
+// weights keep 11 bits down to 2^-43 of such a key's.
 template <int D>
 __device__ __noinline__ MarkedSum zeros_step(RowSum r, const Step st, const int *words, int shift) {
   uint32_t z[4];

@@ -22,10 +22,13 @@ largest terms, of what a row sees only:
   floor     a weight's smallest step is 2^-10 / 16^(parts - 1) / 2^8 of C = max_j p_j 2^ev_j, the largest
     weight times V scale (rows of zeros, which add nothing, do not count); in the chunk kernel
     2^-25 / 2^4 of C' = max_j p_j 2^et_j, et_j the largest V scale of the key's 128 (64 at
-    head_dim 256) but at most 2^15 ev_j.  Times sum_j |code_j|.
+    head_dim 256) but at most 2^15 ev_j, rows of zeros with 2^-24 of their weight.  Times sum_j |code_j|.
   values    fp32 sums over the keys: kv / 16 + 16 additions of one ulp (2 u)
   out       |out - ref| <= u_out |ref| + A (2 ds + parts + the weights' terms + the sums') + floor
             with A = sum_j p_j |v_j|;  |lse - ref| <= ds + 2^-21 + 4 u |lse| (+ kv / 64 u: its sum)
+            + in the chunk kernel, whose exp2's argument is the weight's distance from the row's units, rounded once:
+            u ln2 times its largest size: 11 (2^5 at the unit, 2^6 above it) and how far a tile's
+            scale is from the unit, 24 above it with rows of zeros, up to 64 below by the spread of the scales
 """
 from __future__ import annotations
 
@@ -105,13 +108,18 @@ def attend(pr):
                     live = torch.where(codes > 0, ev, torch.tensor(-math.inf, dtype=ev.dtype))
                     tiles = torch.nn.functional.pad(live, (0, -b % bn), value=-math.inf).view(-1, bn).amax(-1)
                     et = torch.minimum(tiles.repeat_interleave(bn)[:b], ev + 15)
-                    c = torch.exp2(((xm - m[:, None]) * LOG2E + et).masked_fill(~counts, -math.inf).amax(-1)) / total
+                    z = torch.where(codes > 0, et, tiles.repeat_interleave(bn)[:b] - 24)
+                    c = torch.exp2(((xm - m[:, None]) * LOG2E + z).masked_fill(~seen, -math.inf).amax(-1)) / total
                 floor = step * c * (seen.double() @ codes)
                 big_a = p @ vh.abs()
                 rel = 2 * ds + parts + ew + (b / 16 + 16) * 2 * U
                 tol_o[at:at + a, h] = half * out[at:at + a, h].nan_to_num(0.0).abs() + big_a * rel[:, None] + floor[:, None] + 1e-37
                 l = lse[at:at + a, h].nan_to_num(0.0, 0.0, 0.0).abs()
-                tol_l[at:at + a, h] = torch.where(some, ds + 2.0 ** -21 + 4 * U * l + b / 64 * U, 0.0)
+                far = 0.0
+                if not few:
+                    real = ev[codes > 0]
+                    far = 11 + (24 if (codes == 0).any() else 0) + (min(64, (real.max() - real.min()).item()) if len(real) else 0)
+                tol_l[at:at + a, h] = torch.where(some, ds + 2.0 ** -21 + 4 * U * l + (b / 64 + math.log(2) * far) * U, 0.0)
         at += a
     return out, lse, tol_o, tol_l
 
