@@ -522,16 +522,18 @@ RPA_API int rpa_q8_workspace_size(const rpa_dims *dims, int32_t max_seqs,
  *   q.k_j) with k_j, v_j the values that the cached rows stand for, taken as
  *   they are.  Sums, maxima and lse are held in fp32 and out is rounded once;
  *   what enters the products has fewer bits where dtype is RPA_BF16:
- *     weights  16 rows or fewer per KV head (q_len * G): off by 2^-19 of the weight
- *              at most; more rows: by 2^-11 (fp16).  fp32: by 2^-24 or less
+ *     weights  sequences of q_len * G <= 16 (or q_len 1): off by 2^-19 of the
+ *              weight at most; longer ones: by 2^-11 (fp16).  fp32: by 2^-24
  *     q        exact down to 2^-12 of the row's largest value, and within 2^-21
- *              of that below.  fp32: off by 2^-24 of the value, or 2^-37 of the largest
+ *              of that below.  fp32: off by 2^-24 of the value, or 2^-37 of the
+ *              largest
  *   A weight counts relative to the row's largest weight times V scale, down to
  *   2^-29 of it (2^-38 for fp32).  V rows of zeros, of scale 2^0 as the format has
  *   them, are left out of that (with more than 16 bf16 rows per KV head, as far as
- *   their weights are at most 2^24 times the others' largest).  Weights times values are summed before the division by the weights'
- *   sum: values above 2^120 over the number of keys may overflow, and weights
- *   below 2^-126 of the row's largest or contributions below 2^-110 may be lost.
+ *   their weights are at most 2^24 times the others' largest).  Weights times
+ *   values are summed before the division by the weights' sum: values above
+ *   2^120 over the number of keys may overflow, and weights below 2^-126 of the
+ *   row's largest or contributions below 2^-110 may be lost.
  *   The keys are all in the cache: new tokens are written by rpa_q8_write
  *   first and attended to as stored.  Any kv_len >= 0 is allowed for any
  *   q_len: with causal == 0 this is cross attention to cached states of

@@ -33,9 +33,9 @@
 // Roles (512 threads of at most 128 registers).  Every hot loop is short and
 // rolled: with five kinds of warps on an SM the unrolled forms (a row's 128 scores in
 // registers) were bound by instruction fetch, at a third of this speed.
-// Measured (Hq 32, Hkv 8, D 128): 8 prompts of 2048 tokens 408 us (674 TFLOP/s of the causal
-// products), 4 chunks of 512 behind contexts of some thousands 195 us (725 TFLOP/s); D 256 (Hq 16,
-// Hkv 4), 4 prompts of 4096 tokens 941 us (584 TFLOP/s).  A block of
+// Measured (Hq 32, Hkv 8, D 128): 8 prompts of 2048 tokens 402 us (684 TFLOP/s of the causal
+// products), 4 chunks of 512 behind contexts of some thousands 194 us (725 TFLOP/s); D 256 (Hq 16,
+// Hkv 4), 4 prompts of 4096 tokens 940 us (585 TFLOP/s).  A block of
 // 128 keys takes 4,200 to 4,900 clocks where its MMAs need 2,048: the conversion of its K and V takes
 // the converters 4,200 (1,250 each, the rest waits that are over when they are looked at), a
 // softmax step 2,000 to 2,500 of which the exponentials are 650 to 1,200, by whether both
@@ -50,7 +50,7 @@
 //   warp 13         walks the run: writes its segments down for the others; TMA of Q
 //   warp 14         TMA of the code tiles; the scales of their keys as fp16 factors; looks
 //                   for rows of zeros among those of scale 2^0 (8 prompts of 2048 tokens take
-//                   480 us where every row has that scale, 790 us with a V row of zeros in every block)
+//                   480 us where every row has that scale, 780 us with a V row of zeros in every block)
 // TMEM (512 columns): S/P of tile 0 (two buffers of 64 keys) | of tile 1 | O of
 // tile 0 | O of tile 1.
 #include <cuda.h>

@@ -43,9 +43,9 @@
 // 5 MMA issue, 6 the scales (cp.async).  4 and 6 run ahead across groups through
 // rings in shared memory.
 //
-// Measured: 128 single tokens behind 1024 to 8192 keys (Hq 32, Hkv 8, D 128) 168 us, 5.9 TB/s of
-// the cache's bytes, 0.90 of a plain copy's rate (986 MB read where 985 are needed); contexts up to
-// 131072 at D 256 320 us, 6.7 TB/s.  fp32 single tokens of the same lengths run at 5.3 TB/s; every
+// Measured: 128 single tokens behind 1024 to 8192 keys (Hq 32, Hkv 8, D 128) 158 to 168 us by the
+// card, 5.9 to 6.2 TB/s of the cache's bytes, 0.90 to 0.95 of a plain copy's rate (986 MB read where 985 are needed); contexts up to
+// 131072 at D 256 315 to 320 us, 6.7 to 6.8 TB/s.  fp32 single tokens of the same lengths run at 5.3 TB/s; every
 // 8 fp32 rows of a KV head pass over its keys once more (4 chunks of 512 behind contexts 2.3 ms).
 #include <cuda.h>
 #include <limits.h>
